@@ -418,6 +418,111 @@ moe_status_t dense_ffn_bf16(int32_t H, int32_t I, float limit, const uint16_t* x
 moe_status_t nvfp4_dequant(const uint8_t* codes, const uint8_t* scales, const float* tensor_scale,
                            int32_t rows, int32_t K, float* out, void* stream);
 
+/* ------------------------------------------------- router balance, gradients */
+
+/*
+ * Balance loss of the router with the experts' assignment counts, per
+ * sequence -- no counterpart in the pages, whose router is balanced by its
+ * correction bias alone; it is what a user who trains the router adds to the
+ * objective. With s = sigmoid(logits), S_t = sum_e s_te, and for sequence b of
+ * T_b tokens
+ *   counts[b, e]      = assignments of its tokens to expert e
+ *   mean_scores[b, e] = 1/T_b sum_t s_te / S_t
+ *   loss[b]           = coef * sum_e f_be mean_scores[b, e],
+ *                       f_be = E counts[b, e] / (k T_b)
+ *   logits      fp32 [T, E] (moe_router_topk's)
+ *   ids         int32 [T, k] (moe_router_topk's); an id outside [0, E) marks a
+ *               dropped assignment and is not counted
+ *   seq_offsets int32 [num_seqs + 1], ascending rows in [0, T]: sequence b is
+ *               rows seq_offsets[b] .. seq_offsets[b+1] - 1 and may be empty
+ *               (counts, scores and loss 0); rows outside all sequences are
+ *               ignored. NULL: one sequence of all T rows (num_seqs must be
+ *               1). Offsets that break this order give unspecified results;
+ *               every access stays in bounds.
+ *   counts int32 [num_seqs, E], mean_scores fp32 [num_seqs, E], loss fp32
+ *   [num_seqs]: out.
+ *   ws: moe_balance_workspace_size bytes, contents need no initialisation.
+ * A row whose scores sum to 0 adds nothing to mean_scores; a NaN logit makes
+ * its sequence's mean_scores and loss NaN. All of the FULL expert count is
+ * counted (local range ignored). T = 0 writes zeros. The order of every sum is
+ * fixed: equal inputs give equal bits.
+ */
+size_t moe_balance_workspace_size(const moe_config_t* cfg, int32_t T, int32_t num_seqs);
+moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,
+                              const int32_t* seq_offsets, int32_t num_seqs, float coef, int32_t* counts,
+                              float* mean_scores, float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the logits from the routing weights of moe_router_topk
+ * (d_weights) and from moe_balance_loss (d_loss), in one pass:
+ *   d_s_te  = d_loss[b] coef / (T_b S_t) (f_be - sum_j f_bj s_tj / S_t)
+ *             + sum over slots j with ids[t, j] = e of
+ *               rsf / C_t (d_weights[t, j] - sum_i d_weights[t, i] s_i / C_t)
+ *   d_logits[t, e] = d_s_te s_te (1 - s_te)
+ * where C_t is the sum of the chosen experts' scores. The counts carry no
+ * gradient; selection (ids) is a constant.
+ *   logits, ids, seq_offsets, num_seqs, coef: as for moe_balance_loss; ids
+ *               outside [0, E) take no part
+ *   d_weights   fp32 [T, k], NULL = no such term
+ *   counts      int32 [num_seqs, E] of moe_balance_loss, d_loss fp32
+ *               [num_seqs]; both NULL = no balance term
+ *   d_logits    out fp32 [T, E]; rows outside all sequences are left as they
+ *               were
+ * A zero score sum (S_t or C_t) gives zero for its term. At least one of
+ * d_weights and d_loss is required. Needs no workspace.
+ */
+moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,
+                                 const float* d_weights, const int32_t* seq_offsets, int32_t num_seqs, float coef,
+                                 const int32_t* counts, const float* d_loss, float* d_logits, void* stream);
+
+/* --------------------------------------------------------- BF16 linear layer */
+
+/* Activation of linear_bf16. GELU is the exact form z Phi(z), GELU_TANH its
+ * tanh approximation, SILU z / (1 + e^-z). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 } moe_act_t;
+
+/*
+ * BF16 linear layer with a fused epilogue -- the product that dense_ffn_bf16
+ * is built of, for every projection around the site:
+ *   z = x w^T + bias;  y = act(z) + residual
+ *   x bf16 [T, K], w bf16 [N, K], bias bf16 [N] or NULL, residual bf16 [T, N]
+ *   or NULL, z_out bf16 [T, N] or NULL (the pre-activation, kept for
+ *   linear_bf16_backward), y bf16 [T, N]. fp32 accumulation and epilogue, one
+ *   rounding each for z_out and y (y comes from the unrounded z).
+ *   ldx, ldw, ldr, ldz, ldy: row pitches in elements (>= K or N). Any pitch
+ *   and any K, N >= 1 is accepted; x or w rows whose pitch is not a multiple
+ *   of 8 elements are first copied to one that is, in the workspace. residual
+ *   and y may be the same tensor with the same pitch; other overlaps of inputs
+ *   and outputs are not allowed.
+ *   ws: linear_workspace_size(T, K, N, ldx, ldw) bytes (0 on invalid
+ *   arguments), contents need no initialisation; its first 4 bytes are a
+ *   device status word (moe_read_device_status). Calls that may overlap on the
+ *   GPU need workspaces of their own.
+ * The order of every sum is fixed: equal inputs give equal bits. A row's
+ * result may depend on T in its last bit (the split of the reduction does).
+ */
+size_t linear_workspace_size(int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw);
+moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T, int32_t K, const uint16_t* w,
+                         int64_t ldw, int32_t N, const uint16_t* bias, const uint16_t* residual, int64_t ldr,
+                         uint16_t* z_out, int64_t ldz, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Gradients of linear_bf16:
+ *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  db = sum_t dz
+ *   dy bf16 [T, N]; z bf16 [T, N], the pre-activation linear_bf16 kept (NULL
+ *   with MOE_ACT_NONE); dx bf16 [T, K], dw bf16 [N, K], db fp32 [N]: out, each
+ *   may be NULL, not all. The residual's gradient is dy itself. dz enters the
+ *   two products rounded to bf16 and db unrounded; accumulation is fp32.
+ *   Pitches as above. T = 0 writes zeros to dw and db.
+ *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above.
+ */
+size_t linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw);
+moe_status_t linear_bf16_backward(int32_t act, const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
+                                  const uint16_t* x, int64_t ldx, int32_t T, int32_t K, const uint16_t* w,
+                                  int64_t ldw, int32_t N, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw,
+                                  float* db, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ whole site */
 
 /*

@@ -21,6 +21,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_TIMEOUT", 6: "MOE_ERR_DEVICE_BOUNDS"}
 PATH_DECODE, PATH_PREFILL, PATH_PREFILL_W4A16 = 0, 1, 2
 PROJ_GATE_UP, PROJ_DOWN = 0, 1
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # every symbol include/routed_nvfp4.h declares
 EXPORTED = (
@@ -30,6 +31,8 @@ EXPORTED = (
     "moe_set_stage_events", "moe_forward_decode_noalloc", "moe_padded_rows", "moe_prepared_size",
     "moe_prepare_weights", "nvfp4_quantize_rows", "nvfp4_grouped_gemm", "moe_unpermute", "moe_unpermute_combine",
     "moe_combine_f32", "moe_noalloc_read_device_status", "moe_set_wait_limit", "nvfp4_grouped_gemm_w4a16",
+    "moe_balance_workspace_size", "moe_balance_loss", "moe_router_backward", "linear_workspace_size", "linear_bf16",
+    "linear_backward_workspace_size", "linear_bf16_backward",
 )
 STAGES = ("router_logits", "topk", "permute", "act_quant", "expert_gate_up", "h_quant", "expert_down", "shared",
           "combine")
@@ -75,7 +78,7 @@ def load_library(path: str = _LIB_PATH) -> C.CDLL:
         raise RuntimeError(f"CUDA library {path} is missing: build it with "
                            f"`python -m routed_nvfp4_expert_b200.build` (there is no CPU fallback)")
     lib = C.CDLL(path)
-    i32, sz, vp, st = C.c_int32, C.c_size_t, C.c_void_p, C.c_int
+    i32, i64, sz, vp, st = C.c_int32, C.c_int64, C.c_size_t, C.c_void_p, C.c_int
     cfgp = C.POINTER(MoeConfig)
     sig = {
         "moe_workspace_size": (sz, [cfgp, i32, i32]),
@@ -108,6 +111,14 @@ def load_library(path: str = _LIB_PATH) -> C.CDLL:
                                     vp, sz, vp]),
         "moe_unpermute": (st, [cfgp, vp, i32, C.POINTER(MoePlan), vp, vp, vp]),
         "moe_unpermute_combine": (st, [cfgp, vp, i32, C.POINTER(MoePlan), vp, vp, vp, vp]),
+        "moe_balance_workspace_size": (sz, [cfgp, i32, i32]),
+        "moe_balance_loss": (st, [cfgp, vp, vp, i32, vp, i32, C.c_float, vp, vp, vp, vp, sz, vp]),
+        "moe_router_backward": (st, [cfgp, vp, vp, i32, vp, vp, i32, C.c_float, vp, vp, vp, vp]),
+        "linear_workspace_size": (sz, [i32, i32, i32, i64, i64]),
+        "linear_bf16": (st, [i32, vp, i64, i32, i32, vp, i64, i32, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp]),
+        "linear_backward_workspace_size": (sz, [i32, i32, i32, i64, i64]),
+        "linear_bf16_backward": (st, [i32, vp, i64, vp, i64, vp, i64, i32, i32, vp, i64, i32, vp, i64, vp, i64, vp,
+                                      vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -341,6 +352,136 @@ def moe_unpermute(cfg: SiteConfig, rows, T: int, plan: MoePlan, ids, out, stream
 def moe_unpermute_combine(cfg: SiteConfig, rows, T: int, plan: MoePlan, ids, shared, y, stream=None):
     _check(lib().moe_unpermute_combine(C.byref(cfg.c()), _p(rows), T, C.byref(plan), _p(ids), _p(shared), _p(y),
                                        _stream(stream)))
+
+
+# ------------------------------------------------------------------ router balance and gradients
+
+def _arg(t, name: str, dtype, shape) -> int | None:
+    """Pointer of a contiguous tensor on the current device with this dtype and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    _same_device(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _same_device(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _seqs(seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
+        raise ValueError("seq_offsets: expected num_seqs + 1 offsets")
+    return seq_offsets.numel() - 1
+
+
+def alloc_balance_workspace(cfg: SiteConfig, T: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
+    n = lib().moe_balance_workspace_size(C.byref(cfg.c()), T, num_seqs)
+    if n == 0:
+        raise MoEError(1, lib().moe_last_error().decode())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_balance_loss(cfg: SiteConfig, logits, ids, coef: float, counts, mean_scores, loss, ws, seq_offsets=None,
+                     stream=None):
+    """logits fp32 [T, E], ids int32 [T, k] -> counts int32 [B, E], mean_scores
+    fp32 [B, E], loss fp32 [B] (B sequences of seq_offsets int32 [B + 1], one
+    when it is None)."""
+    T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().moe_balance_loss(
+        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E)), _arg(ids, "ids", i32, (T, k)), T,
+        _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, coef, _arg(counts, "counts", i32, (B, E)),
+        _arg(mean_scores, "mean_scores", f32, (B, E)), _arg(loss, "loss", f32, (B,)), _p(ws), ws.numel(),
+        _stream(stream)))
+
+
+def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, coef: float = 0.0, counts=None,
+                        d_loss=None, seq_offsets=None, stream=None):
+    """Gradient of the logits from the routing weights (d_weights fp32 [T, k])
+    and the balance loss (counts of moe_balance_loss and d_loss fp32 [B])."""
+    T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().moe_router_backward(
+        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E)), _arg(ids, "ids", i32, (T, k)), T,
+        _arg(d_weights, "d_weights", f32, (T, k)), _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, coef,
+        _arg(counts, "counts", i32, (B, E)), _arg(d_loss, "d_loss", f32, (B,)),
+        _arg(d_logits, "d_logits", f32, (T, E)), _stream(stream)))
+
+
+# ------------------------------------------------------------------ BF16 linear layer
+
+def _rows(t, name: str, shape):
+    """(pointer, row pitch) of a bf16 matrix whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected torch.bfloat16 {shape}, got {t.dtype} {tuple(t.shape)}")
+    _same_device(t, name)
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    return t.data_ptr(), max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
+    return ACTIVATIONS[act]
+
+
+def _alloc_linear(size, x, w) -> torch.Tensor:
+    (T, K), N = x.shape, w.shape[0]
+    n = size(T, K, N, _rows(x, "x", (T, K))[1], _rows(w, "w", (N, K))[1])
+    if n == 0:
+        raise MoEError(1, lib().moe_last_error().decode())
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def alloc_linear_workspace(x, w) -> torch.Tensor:
+    """Workspace of linear_bf16 for operands of these shapes and strides."""
+    return _alloc_linear(lib().linear_workspace_size, x, w)
+
+
+def alloc_linear_backward_workspace(dy, x, w) -> torch.Tensor:
+    """Workspace of linear_bf16_backward for operands of these shapes and strides."""
+    return _alloc_linear(lib().linear_backward_workspace_size, x, w)
+
+
+def linear_bf16(x, w, y, ws, bias=None, residual=None, act: str = "none", z=None, stream=None):
+    """y = act(x w^T + bias) + residual; z receives the pre-activation. x [T, K],
+    w [N, K], bias [N], residual, z, y [T, N], all bf16; rows may be strided."""
+    (T, K), N = x.shape, w.shape[0]
+    xp, ldx = _rows(x, "x", (T, K))
+    wp, ldw = _rows(w, "w", (N, K))
+    rp, ldr = _rows(residual, "residual", (T, N))
+    zp, ldz = _rows(z, "z", (T, N))
+    yp, ldy = _rows(y, "y", (T, N))
+    _check(lib().linear_bf16(_activation(act), xp, ldx, T, K, wp, ldw, N, _arg(bias, "bias", torch.bfloat16, (N,)), rp,
+                             ldr, zp, ldz, yp, ldy, _p(ws), ws.numel(), _stream(stream)))
+
+
+def linear_bf16_backward(dy, x, w, ws, z=None, act: str = "none", dx=None, dw=None, db=None, stream=None):
+    """dz = dy act'(z); dx = dz w, dw = dz^T x (bf16), db = sum of dz over the
+    tokens (fp32 [N]); each output may be None, not all."""
+    (T, K), N = x.shape, w.shape[0]
+    dyp, lddy = _rows(dy, "dy", (T, N))
+    zp, ldz = _rows(z, "z", (T, N))
+    xp, ldx = _rows(x, "x", (T, K))
+    wp, ldw = _rows(w, "w", (N, K))
+    dxp, lddx = _rows(dx, "dx", (T, K))
+    dwp, lddw = _rows(dw, "dw", (N, K))
+    _check(lib().linear_bf16_backward(_activation(act), dyp, lddy, zp, ldz, xp, ldx, T, K, wp, ldw, N, dxp, lddx, dwp,
+                                      lddw, _arg(db, "db", torch.float32, (N,)), _p(ws), ws.numel(), _stream(stream)))
 
 
 def moe_workspace_views(cfg: SiteConfig, T: int, path: int, ws) -> MoeViews:

@@ -123,6 +123,31 @@ moe_status_t check_T(int32_t T) {
   return MOE_OK;
 }
 
+moe_status_t check_seqs(const int32_t* off, int32_t n, bool sizes_only) {
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "num_seqs=%d is negative", n);
+  if (n > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "num_seqs=%d too large", n);
+  if (sizes_only) return MOE_OK;
+  if (!off && n != 1) return fail(MOE_ERR_INVALID_ARG, "num_seqs=%d without seq_offsets (must be 1)", n);
+  if (off && !aligned16(off)) return fail(MOE_ERR_INVALID_ARG, "seq_offsets is not 16-byte aligned");
+  return MOE_OK;
+}
+
+// Row pitches stay below the tensor map's limit of 2^40 bytes.
+moe_status_t check_pitch(int64_t ld, int32_t cols, const char* name) {
+  if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s=%lld is below the row length %d", name, (long long)ld, cols);
+  if (ld >= (1LL << 38)) return fail(MOE_ERR_UNSUPPORTED, "%s=%lld too large", name, (long long)ld);
+  return MOE_OK;
+}
+
+moe_status_t check_linear(int32_t act, int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw) {
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (T < 0 || K < 1 || N < 1) return fail(MOE_ERR_INVALID_ARG, "T=%d K=%d N=%d: need T >= 0, K >= 1, N >= 1", T, K, N);
+  if (T > (1 << 23) || K > (1 << 23) || N > (1 << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "T=%d K=%d N=%d: at most 2^23 each", T, K, N);
+  moe_status_t s = check_pitch(ldx, K, "ldx");
+  return s != MOE_OK ? s : check_pitch(ldw, K, "ldw");
+}
+
 moe_status_t check_bank(const nvfp4_bank_t& b, const char* name) {
   char buf[64];
   snprintf(buf, sizeof buf, "%s.codes", name);
@@ -743,6 +768,141 @@ moe_status_t dense_ffn_bf16(int32_t H, int32_t I, float limit, const uint16_t* x
   cudaStream_t st = (cudaStream_t)stream;
   RNX_CUDA(cudaMemsetAsync(ws, 0, 4, st), "clear status");
   RNX_CUDA(rnx::launch_dense_ffn(H, I, limit, x, T, wg, wu, wd, y, false, hbuf, (uint32_t*)ws, st), "dense_ffn_bf16");
+  return MOE_OK;
+}
+
+size_t moe_balance_workspace_size(const moe_config_t* cfg, int32_t T, int32_t num_seqs) {
+  if (check_cfg(cfg) != MOE_OK || check_T(T) != MOE_OK || check_seqs(nullptr, num_seqs, true) != MOE_OK) return 0;
+  const size_t blocks = rnx::balance_blocks(T);
+  return up(blocks ? 8 * (blocks + num_seqs) * (size_t)cfg->num_experts : 1);
+}
+
+moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,
+                              const int32_t* seq_offsets, int32_t num_seqs, float coef, int32_t* counts,
+                              float* mean_scores, float* loss, void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t s;
+  if ((s = check_cfg(cfg)) != MOE_OK || (s = check_T(T)) != MOE_OK ||
+      (s = check_seqs(seq_offsets, num_seqs, false)) != MOE_OK)
+    return s;
+  if (!std::isfinite(coef)) return fail(MOE_ERR_INVALID_ARG, "coef is not finite");
+  if (num_seqs == 0) return MOE_OK;
+  if (T > 0) {
+    RNX_PTR(logits, "logits");
+    RNX_PTR(ids, "ids");
+  }
+  RNX_PTR(counts, "counts");
+  RNX_PTR(mean_scores, "mean_scores");
+  RNX_PTR(loss, "loss");
+  if (!ws || ((uintptr_t)ws % kAlign)) return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
+  const size_t need = moe_balance_workspace_size(cfg, T, num_seqs);
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  RNX_CUDA(rnx::launch_balance_loss(logits, ids, T, cfg->num_experts, cfg->top_k, seq_offsets, num_seqs, coef, counts,
+                                    mean_scores, loss, ws, (cudaStream_t)stream),
+           "moe_balance_loss");
+  return MOE_OK;
+}
+
+moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,
+                                 const float* d_weights, const int32_t* seq_offsets, int32_t num_seqs, float coef,
+                                 const int32_t* counts, const float* d_loss, float* d_logits, void* stream) {
+  moe_status_t s;
+  if ((s = check_cfg(cfg)) != MOE_OK || (s = check_T(T)) != MOE_OK ||
+      (s = check_seqs(seq_offsets, num_seqs, false)) != MOE_OK)
+    return s;
+  if (!std::isfinite(coef)) return fail(MOE_ERR_INVALID_ARG, "coef is not finite");
+  if (!d_weights && !d_loss) return fail(MOE_ERR_INVALID_ARG, "d_weights and d_loss are both NULL");
+  if (!d_loss != !counts) return fail(MOE_ERR_INVALID_ARG, "d_loss and counts go together: one of them is NULL");
+  if (T == 0 || num_seqs == 0) return MOE_OK;
+  RNX_PTR(logits, "logits");
+  if (d_weights) {
+    RNX_PTR(d_weights, "d_weights");
+    RNX_PTR(ids, "ids");
+  }
+  if (d_loss) {
+    RNX_PTR(d_loss, "d_loss");
+    RNX_PTR(counts, "counts");
+  }
+  RNX_PTR(d_logits, "d_logits");
+  RNX_CUDA(rnx::launch_router_grad(logits, ids, T, cfg->num_experts, cfg->top_k, d_weights,
+                                   cfg->routed_scaling_factor, seq_offsets, num_seqs, coef, counts, d_loss, d_logits,
+                                   (cudaStream_t)stream),
+           "moe_router_backward");
+  return MOE_OK;
+}
+
+size_t linear_workspace_size(int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw) {
+  if (check_linear(MOE_ACT_NONE, T, K, N, ldx, ldw) != MOE_OK) return 0;
+  return rnx::linear_layout(T, K, N, ldx, ldw).bytes;
+}
+
+size_t linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw) {
+  if (check_linear(MOE_ACT_NONE, T, K, N, ldx, ldw) != MOE_OK) return 0;
+  return rnx::linear_backward_layout(T, K, N, ldx, ldw).bytes;
+}
+
+moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T, int32_t K, const uint16_t* w,
+                         int64_t ldw, int32_t N, const uint16_t* bias, const uint16_t* residual, int64_t ldr,
+                         uint16_t* z_out, int64_t ldz, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
+                         void* stream) {
+  moe_status_t s;
+  if ((s = check_linear(act, T, K, N, ldx, ldw)) != MOE_OK) return s;
+  if (T == 0) return MOE_OK;
+  RNX_PTR(x, "x");
+  RNX_PTR(w, "w");
+  RNX_PTR(y, "y");
+  if (bias) RNX_PTR(bias, "bias");
+  if (residual) {
+    RNX_PTR(residual, "residual");
+    if ((s = check_pitch(ldr, N, "ldr")) != MOE_OK) return s;
+  }
+  if (z_out) {
+    RNX_PTR(z_out, "z_out");
+    if ((s = check_pitch(ldz, N, "ldz")) != MOE_OK) return s;
+  }
+  if ((s = check_pitch(ldy, N, "ldy")) != MOE_OK) return s;
+  if (!ws || ((uintptr_t)ws % kAlign)) return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
+  const size_t need = rnx::linear_layout(T, K, N, ldx, ldw).bytes;
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  const rnx::LinearArgs a{T, K, N, x, w, bias, residual, z_out, y, ldx, ldw, ldr, ldz, ldy};
+  RNX_CUDA(rnx::launch_linear(act, a, ws, (cudaStream_t)stream), "linear_bf16");
+  return MOE_OK;
+}
+
+moe_status_t linear_bf16_backward(int32_t act, const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
+                                  const uint16_t* x, int64_t ldx, int32_t T, int32_t K, const uint16_t* w,
+                                  int64_t ldw, int32_t N, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw,
+                                  float* db, void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t s;
+  if ((s = check_linear(act, T, K, N, ldx, ldw)) != MOE_OK) return s;
+  if (!dx && !dw && !db) return fail(MOE_ERR_INVALID_ARG, "dx, dw and db are all NULL");
+  if (dx) {
+    RNX_PTR(dx, "dx");
+    if ((s = check_pitch(lddx, K, "lddx")) != MOE_OK) return s;
+  }
+  if (dw) {
+    RNX_PTR(dw, "dw");
+    if ((s = check_pitch(lddw, K, "lddw")) != MOE_OK) return s;
+  }
+  if (db) RNX_PTR(db, "db");
+  cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {
+    if (dw) RNX_CUDA(cudaMemset2DAsync(dw, 2 * (size_t)lddw, 0, 2 * (size_t)K, N, st), "clear dw");
+    if (db) RNX_CUDA(cudaMemsetAsync(db, 0, 4 * (size_t)N, st), "clear db");
+    return MOE_OK;
+  }
+  RNX_PTR(dy, "dy");
+  if ((s = check_pitch(lddy, N, "lddy")) != MOE_OK) return s;
+  if (act != MOE_ACT_NONE) {
+    RNX_PTR(z, "z");
+    if ((s = check_pitch(ldz, N, "ldz")) != MOE_OK) return s;
+  }
+  if (dw) RNX_PTR(x, "x");
+  if (dx) RNX_PTR(w, "w");
+  if (!ws || ((uintptr_t)ws % kAlign)) return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
+  const size_t need = rnx::linear_backward_layout(T, K, N, ldx, ldw).bytes;
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  const rnx::LinearBackwardArgs a{T, K, N, dy, z, x, w, dx, dw, db, lddy, ldz, ldx, ldw, lddx, lddw};
+  RNX_CUDA(rnx::launch_linear_backward(act, a, ws, st), "linear_bf16_backward");
   return MOE_OK;
 }
 

@@ -292,4 +292,49 @@ struct W4a16GemmArgs {
 };
 cudaError_t launch_w4a16_grouped_gemm(const W4a16GemmArgs& a, cudaStream_t st);
 
+// ---------------------------------------------------------------- router balance (balance.cu)
+
+// Inputs of up to this many tokens are summed by one CTA per sequence (one
+// launch); longer ones by one CTA per SM and a join.
+constexpr int kBalanceSeqMaxT = 256;
+// CTAs of the first step of launch_balance_loss (0: the one-launch form); its
+// scratch holds (blocks + B) * E floats and as many ints.
+int balance_blocks(int T);
+// off: [B + 1] ascending row offsets (NULL with B = 1: all T rows).
+cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
+                                int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
+                                cudaStream_t st);
+// d_weights NULL: no routing-weight term; d_loss NULL: no balance term.
+cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, int E, int k, const float* d_weights,
+                               float rsf, const int32_t* off, int B, float coef, const int32_t* counts,
+                               const float* d_loss, float* d_logits, cudaStream_t st);
+
+// ---------------------------------------------------------------- BF16 linear layer (linear.cu)
+
+constexpr int kLinearMaxSmem = 226 * 1024;   // opt-in limit of 227 KB less the kernels' static barriers
+
+// Workspace offsets: the status word, then what the call needs of copies of x
+// and w in 16-byte-aligned rows, dz and the partial column sums of db.
+struct LinearLayout {
+  size_t x, w, dz, part, bytes;
+};
+LinearLayout linear_layout(int T, int K, int N, long long ldx, long long ldw);
+LinearLayout linear_backward_layout(int T, int K, int N, long long ldx, long long ldw);
+
+struct LinearArgs {
+  int T, K, N;
+  const uint16_t *x, *w, *bias, *residual;   // bias, residual nullable
+  uint16_t *z, *y;                           // z nullable
+  long long ldx, ldw, ldr, ldz, ldy;         // row pitches in elements
+};
+struct LinearBackwardArgs {
+  int T, K, N;
+  const uint16_t *dy, *z, *x, *w;            // z unused without an activation
+  uint16_t *dx, *dw;                         // nullable
+  float* db;                                 // nullable
+  long long lddy, ldz, ldx, ldw, lddx, lddw;
+};
+cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t st);
+cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* ws, cudaStream_t st);
+
 }  // namespace rnx

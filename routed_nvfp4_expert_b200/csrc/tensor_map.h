@@ -21,15 +21,15 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// 2D tensor [rows, cols] (cols contiguous, row pitch cols * esz bytes), box
-// box_cols x box_rows, zero fill out of bounds.
+// 2D tensor [rows, cols] (cols contiguous, row pitch `pitch` elements, cols if
+// 0), box box_cols x box_rows, zero fill out of bounds.
 inline bool make_tensor_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, uint64_t esz,
                                uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
-                               CUtensorMapSwizzle swizzle) {
+                               CUtensorMapSwizzle swizzle, uint64_t pitch = 0) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * esz};
+  cuuint64_t strides[1] = {(pitch ? pitch : cols) * esz};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
