@@ -304,6 +304,412 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   }
 }
 
+// ---------------------------------------------------------------- pair kernel
+// Many rows: 256 x bn tiles (bn = 256 or 128) on CTA pairs, out[m, n] with the
+// token (or dW's row) on the accumulator's lanes. One persistent pair per two
+// SMs walks the tiles; the even CTA issues M = 256 MMAs (cta_group::2) on
+// operands both CTAs load, so each CTA brings its 128 rows of A and half of B.
+// Two accumulators of 256 columns fill the tensor memory, so that one tile's
+// epilogue runs beside the next tile's products.
+//
+// Up to two products share a launch: dx and dW depend on dz alone, and their
+// tiles in one list leave one ragged last round instead of two.
+// Warps: 0 = TMA producer, 1 = MMA issuer (even CTA), 2 = TMEM allocator, 3 =
+// db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
+// 64 columns at a time go through a swizzled 32-row box in shared memory, so
+// that global loads and stores are whole 128-byte lines whatever the pitch.
+// Every wait is bounded. No TMA load uses cluster multicast.
+
+constexpr int kPairM = 256;
+constexpr int kPairStages = 6;
+constexpr int kPairBBytes = 128 * 128;                       // half of B's 256 rows
+constexpr int kPairStageBytes = kABytes + kPairBBytes;       // 32 KB
+constexpr int kFirstEpiWarp = 4, kEpiWarps = 8;
+constexpr int kPairThreads = (kFirstEpiWarp + kEpiWarps) * 32;
+constexpr int kEpiBox = 32 * 128;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kEpiBox + 1024;
+constexpr uint32_t kPairTmemCols = 512;
+constexpr int kRaster = 8;                                   // m tiles per raster group
+static_assert(kPairSmem <= kLinearMaxSmem, "shared memory");
+
+struct PairProblem {
+  CUtensorMap tma_a, tma_b;
+  Epilogue ep;
+  int M, N;
+  int ksteps;
+  int a_mn, b_mn;
+  int mt, nt;                 // tiles
+};
+struct PairParams {
+  PairProblem prob[2];
+  DbJoin db;
+  uint32_t* status;
+  int bn;
+  int tiles0, tiles1;         // tiles of the two products (0: absent)
+  int rounds1;                // rounds of the second product in which every pair takes a tile; behind them
+                              // only pairs with fewer tiles of the first do (pairs >= first_light)
+  int first_light;
+  int clear;
+};
+
+// The i-th tile of a pair: first the first product's, round robin, then the
+// second's. Returns false behind the last.
+struct PairTile {
+  int which, index;
+};
+RNX_DEVICE bool pair_tile(const PairParams& p, int pair, int n_pairs, int i, PairTile& t) {
+  const int n0 = pair < p.tiles0 ? (p.tiles0 - pair + n_pairs - 1) / n_pairs : 0;
+  if (i < n0) {
+    t.which = 0;
+    t.index = pair + i * n_pairs;
+    return true;
+  }
+  const int r = i - n0;
+  t.which = 1;
+  if (r < p.rounds1) {
+    t.index = r * n_pairs + pair;
+  } else {
+    if (pair < p.first_light) return false;
+    t.index = p.rounds1 * n_pairs + (r - p.rounds1) * (n_pairs - p.first_light) + pair - p.first_light;
+  }
+  return t.index < p.tiles1;
+}
+
+// Groups of kRaster m tiles, n across: the tiles at work at any time share a
+// few rows of A and of B, which then come from L2.
+RNX_DEVICE void pair_tile_coords(const PairProblem& q, int index, int& mt, int& nt) {
+  const int per = kRaster * q.nt;
+  const int g = index / per, in = index - g * per;
+  const int rows = min(kRaster, q.mt - g * kRaster);
+  nt = in / rows;
+  mt = g * kRaster + (in - nt * rows);
+}
+
+// A warp's box of 32 rows x 64 bf16: 16-byte chunk c of row r at position
+// c ^ (r & 7), so that a lane walking its own row and eight lanes walking one
+// row both reach all banks.
+RNX_DEVICE uint8_t* box_at(uint8_t* box, int row, int chunk) { return box + row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
+  return reinterpret_cast<uint16_t*>(box_at(box, row, col >> 3)) + (col & 7);
+}
+
+// rows x cols of the box to global memory (whole warp). vec: 16-byte rows.
+RNX_DEVICE void box_store(uint8_t* box, uint16_t* dst, long long ld, int rows, int cols, int vec, int lane) {
+  __syncwarp();
+  if (vec) {
+    const int c = lane & 7, left = cols - 8 * c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r < rows && left > 0) {
+        uint16_t* p = dst + r * ld + 8 * c;
+        if (left >= 8)
+          *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(box_at(box, r, c));
+        else
+          for (int e = 0; e < left; ++e) p[e] = *box_elem(box, r, 8 * c + e);
+      }
+    }
+  } else {
+    for (int r = 0; r < rows; ++r) {
+      uint16_t* p = dst + r * ld;
+      if (lane < cols) p[lane] = *box_elem(box, r, lane);
+      if (lane + 32 < cols) p[lane + 32] = *box_elem(box, r, lane + 32);
+    }
+  }
+  __syncwarp();
+}
+
+// The residual's box, in flight in registers (vec) while the accumulator is
+// waited for.
+struct BoxLoad {
+  uint4 v[8];
+};
+RNX_DEVICE void box_issue(BoxLoad& b, const uint16_t* src, long long ld, int rows, int cols, int lane) {
+  const int c = lane & 7, left = cols - 8 * c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    b.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && left >= 8) {
+      b.v[i] = *reinterpret_cast<const uint4*>(src + r * ld + 8 * c);
+    } else if (r < rows && left > 0) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) w[e >> 1] |= (uint32_t)src[r * ld + 8 * c + e] << (16 * (e & 1));
+      b.v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(box_at(box, 4 * i + (lane >> 3), lane & 7)) = b.v[i];
+  __syncwarp();
+}
+RNX_DEVICE void box_load_scalar(uint8_t* box, const uint16_t* src, long long ld, int rows, int cols, int lane) {
+  for (int r = 0; r < rows; ++r) {
+    const uint16_t* p = src + r * ld;
+    if (lane < cols) *box_elem(box, r, lane) = p[lane];
+    if (lane + 32 < cols) *box_elem(box, r, lane + 32) = p[lane + 32];
+  }
+  __syncwarp();
+}
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t full_bar[kPairStages], empty_bar[kPairStages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int half = p.bn / 2;                       // this CTA's rows of B
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&mma_done, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&s_tmem, kPairTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_trigger();
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;   // as in the split kernel
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    int it = 0;
+    bool ok = true;
+    PairTile t;
+    for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i) {
+      const PairProblem& q = p.prob[t.which];
+      int mt, nt;
+      pair_tile_coords(q, t.index, mt, nt);
+      const int am = mt * kPairM + 128 * (int)rank, bn0 = nt * p.bn + half * (int)rank;
+      const int ksteps = q.ksteps, a_mn = q.a_mn, b_mn = q.b_mn;
+      for (int ks = 0; ks < ksteps; ++ks, ++it) {
+        const int s = it % kPairStages;
+        const uint32_t ph = (uint32_t)(it / kPairStages) & 1u;
+        if (__any_sync(0xffffffffu, !mbar_wait_poll(&empty_bar[s], ph ^ 1u) || abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* sA = smem + (size_t)s * kPairStageBytes;
+          uint8_t* sB = sA + kABytes;
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2u * (uint32_t)(kABytes + half * 128));
+          const int k0 = ks * kStepK;
+          if (a_mn) {
+            tma_load_2d_pair(sA, &q.tma_a, am, k0, bar);
+            tma_load_2d_pair(sA + kMnBlock, &q.tma_a, am + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(sA, &q.tma_a, k0, am, bar);
+          }
+          if (b_mn) {
+            tma_load_2d_pair(sB, &q.tma_b, bn0, k0, bar);
+            if (half > 64) tma_load_2d_pair(sB + kMnBlock, &q.tma_b, bn0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(sB, &q.tma_b, k0, bn0, bar);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      set_status(p.status, kDevErrTimeout);
+      abort_flag = 1;
+    }
+    if (rank == 0)     // drain: its full barriers count both CTAs' bytes
+      for (int j = max(0, it - kPairStages); j < it; ++j)
+        if (!mbar_wait(&full_bar[j % kPairStages], (uint32_t)(j / kPairStages) & 1u) && lane == 0)
+          set_status(p.status, kDevErrTimeout);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0) {
+      const uint32_t s0 = smem_u32(smem);
+      int it = 0, tc = 0;
+      bool ok = true;
+      PairTile t;
+      for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
+        const PairProblem& q = p.prob[t.which];
+        const uint32_t idesc = idesc_bf16_major(kPairM, p.bn, q.a_mn, q.b_mn);
+        const uint64_t dA0 = q.a_mn ? sdesc_mn_sw128(s0, kMnBlock) : sdesc_k_sw128(s0);
+        const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
+        const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;
+        const int b = tc & 1, ksteps = q.ksteps;
+        if (__any_sync(0xffffffffu, !mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + 256u * b;
+        for (int ks = 0; ks < ksteps; ++ks, ++it) {
+          const int s = it % kPairStages;
+          const uint32_t ph = (uint32_t)(it / kPairStages) & 1u;
+          if (__any_sync(0xffffffffu, !mbar_wait_poll(&full_bar[s], ph) || abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t so = (uint64_t)((uint32_t)(s * kPairStageBytes) >> 4);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+              mma_bf16_pair(acc, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (ks > 0 || kb > 0) ? 1u : 0u);
+            mma_commit_pair_mc(&empty_bar[s], 0x3);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit_pair_mc(&acc_full[b], 0x3);
+        __syncwarp();
+      }
+      if (!ok && lane == 0) {
+        set_status(p.status, kDevErrTimeout);
+        abort_flag = 1;
+      }
+      if (elect_one()) mma_commit_pair_mc(&mma_done, 0x1);
+      __syncwarp();
+      if (!mbar_wait(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
+    }
+  } else if (warp == 3) {
+    join_db(p.db, blockIdx.x, gridDim.x, lane);
+  } else if (warp >= kFirstEpiWarp) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int qd = warp & 3, ch = (warp - kFirstEpiWarp) >> 2;
+    const uint32_t acc_empty_even[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
+    uint8_t* box = smem + (size_t)kPairStages * kPairStageBytes + (size_t)(warp - kFirstEpiWarp) * kEpiBox;
+    const int chunks = p.bn / 128;                 // 64-column chunks of this warp
+    int tc = 0;
+    PairTile t;
+    for (int i = 0; pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
+      const PairProblem& q = p.prob[t.which];
+      const Epilogue& ep = q.ep;
+      int mt, nt;
+      pair_tile_coords(q, t.index, mt, nt);
+      const int b = tc & 1;
+      const int row0 = mt * kPairM + 128 * (int)rank + qd * 32;
+      const int rows = min(32, q.M - row0);        // <= 0: none of this warp's rows exist
+      bool gone = false;
+      for (int c = 0; c < chunks; ++c) {
+        const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(64, q.N - col0);
+        BoxLoad res;
+        const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
+        if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);
+        if (c == 0) {
+          if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u) || abort_flag)) {
+            gone = true;
+            break;
+          }
+          tc_fence_after();
+        }
+        uint32_t v[64];
+        const uint32_t tq = tmem + 256u * b + ((uint32_t)(qd * 32) << 16) + half * ch + 64 * c;
+        tmem_ld32(tq, v);
+        tmem_ld32(tq + 32, v + 32);
+        tmem_ld_wait();
+        if (c == chunks - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_even[b]);
+        }
+        if (rows <= 0 || cols <= 0) continue;
+        if (ep.bias) {
+#pragma unroll
+          for (int j = 0; j < 64; j += 8) {        // the same 16 bytes for every lane
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (j + 8 <= cols) {
+              const uint4 u = *reinterpret_cast<const uint4*>(ep.bias + col0 + j);
+              w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (j + e < cols) w[e >> 1] |= (uint32_t)ep.bias[col0 + j + e] << (16 * (e & 1));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = bf16x2_to_f32x2(w[e]);
+              v[j + 2 * e] = __float_as_uint(__uint_as_float(v[j + 2 * e]) + f.x);
+              v[j + 2 * e + 1] = __float_as_uint(__uint_as_float(v[j + 2 * e + 1]) + f.y);
+            }
+          }
+        }
+        if (ep.z) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(box_at(box, lane, j)) =
+                make_uint4(pack_bf16x2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
+                           pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
+                           pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
+                           pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
+          box_store(box, ep.z + row0 * ep.ldz + col0, ep.ldz, rows, cols, ep.vec, lane);
+        }
+        if (res_src) {
+          if (ep.vec) box_land(res, box, lane);
+          else box_load_scalar(box, res_src, ep.ldr, rows, cols, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4* at = reinterpret_cast<uint4*>(box_at(box, lane, j));
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = act_of<ACT>(__uint_as_float(v[8 * j + e]));
+          if (res_src) {
+            const uint4 u = *at;
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = bf16x2_to_f32x2(w[e]);
+              y[2 * e] += f.x, y[2 * e + 1] += f.y;
+            }
+          }
+          *at = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                           pack_bf16x2(y[6], y[7]));
+        }
+        box_store(box, ep.out + row0 * ep.ldo + col0, ep.ldo, rows, cols, ep.vec, lane);
+      }
+      if (gone) {
+        if (lane == 0) {
+          set_status(p.status, kDevErrTimeout);
+          abort_flag = 1;
+        }
+        break;
+      }
+    }
+  }
+
+  // no CTA leaves (or frees TMEM) while the pair's MMAs or copies may still
+  // touch its shared or tensor memory
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmemCols);
+  }
+}
+
 // ---------------------------------------------------------------- dz and db
 // dz = dy act'(z) in bf16 and the column sums of each chunk of rows in fp32
 // (rows of a warp in order, then the warps). A CTA owns 256 columns of one
@@ -528,6 +934,78 @@ cudaError_t launch_split(int act, const Operand& a, const Operand& b, int red, c
   return cudaErrorInvalidValue;
 }
 
+// One product out[m, n] = epilogue(sum_r A[m, r] B[n, r]) of a pair launch.
+struct Product {
+  Operand a, b;
+  int red;
+  Epilogue ep;
+};
+
+template <int ACT>
+cudaError_t launch_pair_act(const PairParams& p, int pairs, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(linear_pair_kernel<ACT>, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(linear_pair_kernel<ACT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, p);
+}
+
+cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoin& db, uint32_t* status, bool clear,
+                        cudaStream_t st) {
+  PairParams p;
+  memset(&p, 0, sizeof p);
+  constexpr int kPairs = kNumSMs / 2;
+  long long tiles[2] = {0, 0};
+  for (int i = 0; i < n; ++i) {
+    PairProblem& q = p.prob[i];
+    q.M = prod[i].a.rows;
+    q.N = prod[i].b.rows;
+    q.ksteps = (prod[i].red + kStepK - 1) / kStepK;
+    q.a_mn = prod[i].a.mn;
+    q.b_mn = prod[i].b.mn;
+    q.mt = (q.M + kPairM - 1) / kPairM;
+    q.nt = (q.N + bn - 1) / bn;
+    q.ep = prod[i].ep;
+    tiles[i] = (long long)q.mt * q.nt;
+    if (tiles[i] > 1 << 30) return cudaErrorInvalidValue;
+    if (!operand_map(&q.tma_a, prod[i].a, prod[i].red, kTileM) || !operand_map(&q.tma_b, prod[i].b, prod[i].red, bn / 2))
+      return cudaErrorInvalidValue;
+  }
+  p.tiles0 = (int)tiles[0];
+  p.tiles1 = (int)tiles[1];
+  p.bn = bn;
+  p.db = db;
+  p.status = status;
+  p.clear = clear;
+  const int pairs = (int)std::min<long long>(kPairs, std::max<long long>(tiles[0], tiles[1]));
+  // second product: how many rounds all pairs share before those with a tile
+  // less of the first product go on alone, for the earliest end
+  const long long each = p.tiles0 / pairs, heavy = p.tiles0 % pairs;
+  const long long k0 = p.prob[0].ksteps, k1 = p.prob[1].ksteps;
+  p.first_light = (int)heavy;
+  long long best = -1;
+  for (long long q = 0; q <= (tiles[1] + pairs - 1) / pairs; ++q) {
+    const long long rest = std::max<long long>(0, tiles[1] - q * pairs), light = pairs - heavy;
+    const long long end = std::max((each + (heavy > 0)) * k0 + q * k1, each * k0 + (q + (rest + light - 1) / light) * k1);
+    if (best < 0 || end < best) {
+      best = end;
+      p.rounds1 = (int)q;
+    }
+  }
+  switch (act) {
+    case MOE_ACT_NONE: return launch_pair_act<MOE_ACT_NONE>(p, pairs, st);
+    case MOE_ACT_RELU: return launch_pair_act<MOE_ACT_RELU>(p, pairs, st);
+    case MOE_ACT_GELU: return launch_pair_act<MOE_ACT_GELU>(p, pairs, st);
+    case MOE_ACT_GELU_TANH: return launch_pair_act<MOE_ACT_GELU_TANH>(p, pairs, st);
+    case MOE_ACT_SILU: return launch_pair_act<MOE_ACT_SILU>(p, pairs, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// The width of the pair kernel's tiles for m x n outputs, 0 for the split kernel.
+int pair_width(int m, int n) {
+  return m > 512 && n > 512 ? 256 : 0;
+}
+
 bool vec_ok(const Epilogue& e) {
   return e.ldo % 8 == 0 && (!e.residual || e.ldr % 8 == 0) && (!e.z || e.ldz % 8 == 0);
 }
@@ -606,6 +1084,10 @@ cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t s
   if (e != cudaSuccess) return e;
   Epilogue ep{a.bias, a.residual, a.z, a.y, a.ldr, a.ldz, a.ldy, 0};
   ep.vec = vec_ok(ep);
+  if (const int bn = pair_width(a.T, a.N)) {
+    const Product prod{x, w, a.K, ep};
+    return launch_pair(act, &prod, 1, bn, DbJoin{}, reinterpret_cast<uint32_t*>(base), pk.n == 0, st);
+  }
   return launch_split(act, w, x, a.K, ep, DbJoin{}, reinterpret_cast<uint32_t*>(base), pk.n == 0, st);
 }
 
@@ -661,21 +1143,32 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (a.db) db = DbJoin{part, a.db, chunks, a.N};
   }
-  if (a.dx) {
-    Epilogue ep{nullptr, nullptr, nullptr, a.dx, 0, 0, a.lddx, 0};
+  Product pair[2];
+  int pairs = 0, width = 0;
+  auto product = [&](bool is_dx) {
+    Epilogue ep{nullptr, nullptr, nullptr, is_dx ? a.dx : a.dw, 0, 0, is_dx ? a.lddx : a.lddw, 0};
     ep.vec = vec_ok(ep);
-    e = launch_split(MOE_ACT_NONE, Operand{w, ldw, a.K, true}, Operand{dz, lddz, a.T, false}, a.N, ep, db, status,
-                     clear, st);
+    // out[t, k] = sum_n dz[t, n] w[n, k];  out[n, k] = sum_t dz[t, n] x[t, k]
+    return is_dx ? Product{Operand{dz, lddz, a.T, false}, Operand{w, ldw, a.K, true}, a.N, ep}
+                 : Product{Operand{dz, lddz, a.N, true}, Operand{x, ldx, a.K, true}, a.T, ep};
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (!(i == 0 ? a.dx : a.dw)) continue;
+    const Product q = product(i == 0);
+    if (const int bn = pair_width(q.a.rows, q.b.rows)) {
+      pair[pairs++] = q;
+      width = bn;
+      continue;
+    }
+    // the split kernel's tiles have the product's rows on its j side
+    e = launch_split(MOE_ACT_NONE, q.b, q.a, q.red, q.ep, db, status, clear, st);
     if (e != cudaSuccess) return e;
     db = DbJoin{};
     clear = false;
   }
-  if (a.dw) {
-    Epilogue ep{nullptr, nullptr, nullptr, a.dw, 0, 0, a.lddw, 0};
-    ep.vec = vec_ok(ep);
-    e = launch_split(MOE_ACT_NONE, Operand{x, ldx, a.K, true}, Operand{dz, lddz, a.N, true}, a.T, ep, db, status,
-                     clear, st);
-    if (e != cudaSuccess) return e;
+  if (pairs == 2 && pair[0].red < pair[1].red) std::swap(pair[0], pair[1]);   // the longer tiles first
+  if (pairs) {
+    if ((e = launch_pair(MOE_ACT_NONE, pair, pairs, width, db, status, clear, st)) != cudaSuccess) return e;
     db = DbJoin{};
   }
   if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);
