@@ -31,18 +31,32 @@ namespace {
 
 // ---------------------------------------------------------------- activations
 
+// The forward's epilogue evaluates 2^15 of these per CTA and tile beside the
+// next tile's products, so their instruction count matters: normcdff made the
+// epilogue the longer of the two (60% of the tensor pipe at 4096 x 4096 x
+// 12288). GELU takes erfc from Abramowitz and Stegun 7.1.26 (absolute error
+// 1.5e-7), the others the exponential and division intrinsics; all stay
+// within 2^-20 of |z|, far inside the result's bf16 step.
 template <int ACT>
 RNX_DEVICE float act_of(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (ACT == MOE_ACT_GELU) return z * normcdff(z);
-  if (ACT == MOE_ACT_GELU_TANH) {
-    const float u = 0.7978845608028654f * fmaf(0.044715f * z * z, z, z);
-    return 0.5f * z * (1.f + tanhf(u));
+  if (ACT == MOE_ACT_GELU) {
+    const float x = fabsf(z) * 0.7071067811865476f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                0.254829592f);
+    const float tail = 0.5f * poly * __expf(-x * x);      // 1 - Phi(|z|)
+    return z * (z > 0.f ? 1.f - tail : tail);
   }
-  if (ACT == MOE_ACT_SILU) return z / (1.f + expf(-z));
+  if (ACT == MOE_ACT_GELU_TANH) {                          // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+    return __fdividef(z, 1.f + __expf(-u2));
+  }
+  if (ACT == MOE_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
   return z;
 }
 
+// The slope, for the HBM-bound dz pass.
 template <int ACT>
 RNX_DEVICE float act_grad(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
@@ -65,6 +79,40 @@ constexpr int kStepK = 64;                 // reduction elements per stage: 128 
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * 128;      // 16 KB; K-major: 128 rows; MN-major: two 64-wide blocks of 64 rows
 constexpr int kMnBlock = 64 * 128;         // one MN-major block: 64 r rows of 128 bytes
+
+// Position in a ring of stages: slot and the parity of its current pass.
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  RNX_DEVICE void next(int stages) {
+    if (++slot == stages) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Bounded wait of a whole warp. A producer's loop is part of a stage's round
+// trip (slot freed, copy issued, data, products, slot freed), and the ring
+// just covers that trip, so the common case is one try and one vote; the abort
+// flag is read only when the slot was not ready.
+RNX_DEVICE bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_poll(bar, parity) && !*abort_flag);
+}
+
+// Waits (bounded) until the last `issued` copies of a producer that stopped at
+// `at` have landed: one pass over the slots it filled.
+RNX_DEVICE void ring_drain(uint64_t* full_bar, Ring at, int issued, int stages, uint32_t* status, int lane) {
+  const int n = min(issued, stages);
+  for (int i = 0; i < n; ++i) {
+    if (--at.slot < 0) {
+      at.slot = stages - 1;
+      at.parity ^= 1u;
+    }
+    if (!mbar_wait(&full_bar[at.slot], at.parity) && lane == 0) set_status(status, kDevErrTimeout);
+  }
+}
 
 struct Epilogue {
   const uint16_t* bias;       // per output feature, nullable
@@ -157,30 +205,26 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   if (p.clear && cta == 0 && threadIdx.x == 0) *p.status = 0u;
 
   if (warp == 0) {
-    int it = 0;
+    Ring r;
+    int issued = 0;
     bool ok = true;
-    for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
-      const int s = it % p.stages;
-      const uint32_t ph = (uint32_t)(it / p.stages) & 1u;
-      if (__any_sync(0xffffffffu, !mbar_wait_poll(&empty_bar[s], ph ^ 1u) || abort_flag)) {
-        ok = false;
-        break;
-      }
+    for (int ks = k_lo; ks < k_hi; ++ks, ++issued, r.next(p.stages)) {
+      if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
       if (elect_one()) {
-        uint8_t* sA = smem + (size_t)s * stage_bytes;
+        uint8_t* sA = smem + (size_t)r.slot * stage_bytes;
         uint8_t* sB = sA + kABytes;
-        mbar_arrive_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
+        uint64_t* bar = &full_bar[r.slot];
+        mbar_arrive_expect_tx(bar, (uint32_t)stage_bytes);
         if (p.a_mn) {
-          tma_load_2d(sA, &p.tma_a, m0, ks * kStepK, &full_bar[s]);
-          tma_load_2d(sA + kMnBlock, &p.tma_a, m0 + 64, ks * kStepK, &full_bar[s]);
+          tma_load_2d(sA, &p.tma_a, m0, ks * kStepK, bar);
+          tma_load_2d(sA + kMnBlock, &p.tma_a, m0 + 64, ks * kStepK, bar);
         } else {
-          tma_load_2d(sA, &p.tma_a, ks * kStepK, m0, &full_bar[s]);
+          tma_load_2d(sA, &p.tma_a, ks * kStepK, m0, bar);
         }
         if (p.b_mn) {
-          for (int c = 0; c < p.bn; c += 64)
-            tma_load_2d(sB + c * 128, &p.tma_b, j0 + c, ks * kStepK, &full_bar[s]);
+          for (int c = 0; c < p.bn; c += 64) tma_load_2d(sB + c * 128, &p.tma_b, j0 + c, ks * kStepK, bar);
         } else {
-          tma_load_2d(sB, &p.tma_b, ks * kStepK, j0, &full_bar[s]);
+          tma_load_2d(sB, &p.tma_b, ks * kStepK, j0, bar);
         }
       }
       __syncwarp();
@@ -189,31 +233,24 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
       set_status(p.status, kDevErrTimeout);
       abort_flag = 1;
     }
-    for (int j = max(0, it - p.stages); j < it; ++j)      // every copy issued must have landed
-      if (!mbar_wait(&full_bar[j % p.stages], (uint32_t)(j / p.stages) & 1u) && lane == 0)
-        set_status(p.status, kDevErrTimeout);
+    ring_drain(full_bar, r, issued, p.stages, p.status, lane);
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16_major(kTileM, p.bn, p.a_mn, p.b_mn);
     const uint32_t s0 = smem_u32(smem);
     const uint64_t dA0 = p.a_mn ? sdesc_mn_sw128(s0, kMnBlock) : sdesc_k_sw128(s0);
     const uint64_t dB0 = p.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
     const uint64_t stepA = p.a_mn ? 2048 >> 4 : 32 >> 4, stepB = p.b_mn ? 2048 >> 4 : 32 >> 4;   // K = 16
-    int it = 0;
+    Ring r;
     bool ok = true;
-    for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
-      const int s = it % p.stages;
-      const uint32_t ph = (uint32_t)(it / p.stages) & 1u;
-      if (__any_sync(0xffffffffu, !mbar_wait_poll(&full_bar[s], ph) || abort_flag)) {
-        ok = false;
-        break;
-      }
+    for (int ks = k_lo; ks < k_hi; ++ks, r.next(p.stages)) {
+      if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t so = (uint64_t)((uint32_t)(s * stage_bytes) >> 4);
+        const uint64_t so = (uint64_t)((uint32_t)(r.slot * stage_bytes) >> 4);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
-          mma_bf16(tmem, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (it > 0 || kb > 0) ? 1u : 0u);
-        mma_commit(&empty_bar[s]);
+          mma_bf16(tmem, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (ks > k_lo || kb > 0) ? 1u : 0u);
+        mma_commit(&empty_bar[r.slot]);
       }
       __syncwarp();
     }
@@ -305,7 +342,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 }
 
 // ---------------------------------------------------------------- pair kernel
-// Many rows: 256 x bn tiles (bn = 256 or 128) on CTA pairs, out[m, n] with the
+// Many rows: 256 x bn tiles (bn up to 256) on CTA pairs, out[m, n] with the
 // token (or dW's row) on the accumulator's lanes. One persistent pair per two
 // SMs walks the tiles; the even CTA issues M = 256 MMAs (cta_group::2) on
 // operands both CTAs load, so each CTA brings its 128 rows of A and half of B.
@@ -314,8 +351,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 //
 // Up to two products share a launch: dx and dW depend on dz alone, and their
 // tiles in one list leave one ragged last round instead of two.
-// Warps: 0 = TMA producer, 1 = MMA issuer (even CTA), 2 = TMEM allocator, 3 =
-// db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
+// Warps: 0 and 3 = TMA producers of A and of B, 1 = MMA issuer (even CTA), 2 =
+// TMEM allocator, then db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
 // 64 columns at a time go through a swizzled 32-row box in shared memory, so
 // that global loads and stores are whole 128-byte lines whatever the pitch.
 // Every wait is bounded. No TMA load uses cluster multicast.
@@ -329,7 +366,7 @@ constexpr int kPairThreads = (kFirstEpiWarp + kEpiWarps) * 32;
 constexpr int kEpiBox = 32 * 128;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kEpiBox + 1024;
 constexpr uint32_t kPairTmemCols = 512;
-constexpr int kRaster = 8;                                   // m tiles per raster group
+constexpr int kRaster = 16;                                  // m tiles per raster group
 static_assert(kPairSmem <= kLinearMaxSmem, "shared memory");
 
 struct PairProblem {
@@ -496,41 +533,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_trigger();
   if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;   // as in the split kernel
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
-    int it = 0;
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ TMA producers (both CTAs)
+    const bool is_a = warp == 0;
+    Ring r;
+    int issued = 0;
     bool ok = true;
     PairTile t;
     for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i) {
       const PairProblem& q = p.prob[t.which];
       int mt, nt;
       pair_tile_coords(q, t.index, mt, nt);
-      const int am = mt * kPairM + 128 * (int)rank, bn0 = nt * p.bn + half * (int)rank;
-      const int ksteps = q.ksteps, a_mn = q.a_mn, b_mn = q.b_mn;
-      for (int ks = 0; ks < ksteps; ++ks, ++it) {
-        const int s = it % kPairStages;
-        const uint32_t ph = (uint32_t)(it / kPairStages) & 1u;
-        if (__any_sync(0xffffffffu, !mbar_wait_poll(&empty_bar[s], ph ^ 1u) || abort_flag)) {
-          ok = false;
-          break;
-        }
+      const CUtensorMap* map = is_a ? &q.tma_a : &q.tma_b;
+      const int first = is_a ? mt * kPairM + 128 * (int)rank : nt * p.bn + half * (int)rank;   // row of the operand
+      const int ksteps = q.ksteps;
+      const bool mn = is_a ? q.a_mn : q.b_mn;
+      const bool two = is_a || half > 64;          // MN-major blocks are 64 wide (then half is 64 or 128)
+      const bool expects = is_a && rank == 0;
+      for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
+        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
         if (elect_one()) {
-          uint8_t* sA = smem + (size_t)s * kPairStageBytes;
-          uint8_t* sB = sA + kABytes;
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2u * (uint32_t)(kABytes + half * 128));
-          const int k0 = ks * kStepK;
-          if (a_mn) {
-            tma_load_2d_pair(sA, &q.tma_a, am, k0, bar);
-            tma_load_2d_pair(sA + kMnBlock, &q.tma_a, am + 64, k0, bar);
+          uint8_t* dst = smem + r.slot * kPairStageBytes + (is_a ? 0 : kABytes);
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[r.slot]), 0);
+          if (expects) mbar_arrive_expect_tx(&full_bar[r.slot], 2u * (uint32_t)(kABytes + half * 128));
+          if (mn) {
+            tma_load_2d_pair(dst, map, first, ks * kStepK, bar);
+            if (two) tma_load_2d_pair(dst + kMnBlock, map, first + 64, ks * kStepK, bar);
           } else {
-            tma_load_2d_pair(sA, &q.tma_a, k0, am, bar);
-          }
-          if (b_mn) {
-            tma_load_2d_pair(sB, &q.tma_b, bn0, k0, bar);
-            if (half > 64) tma_load_2d_pair(sB + kMnBlock, &q.tma_b, bn0 + 64, k0, bar);
-          } else {
-            tma_load_2d_pair(sB, &q.tma_b, k0, bn0, bar);
+            tma_load_2d_pair(dst, map, ks * kStepK, first, bar);
           }
         }
         __syncwarp();
@@ -540,15 +570,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       set_status(p.status, kDevErrTimeout);
       abort_flag = 1;
     }
-    if (rank == 0)     // drain: its full barriers count both CTAs' bytes
-      for (int j = max(0, it - kPairStages); j < it; ++j)
-        if (!mbar_wait(&full_bar[j % kPairStages], (uint32_t)(j / kPairStages) & 1u) && lane == 0)
-          set_status(p.status, kDevErrTimeout);
+    // the even CTA's full barriers count both CTAs' copies of A and B
+    if (rank == 0) ring_drain(full_bar, r, issued, kPairStages, p.status, lane);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0) {
       const uint32_t s0 = smem_u32(smem);
-      int it = 0, tc = 0;
+      Ring r;
+      int tc = 0;
       bool ok = true;
       PairTile t;
       for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
@@ -558,26 +587,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
         const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;
         const int b = tc & 1, ksteps = q.ksteps;
-        if (__any_sync(0xffffffffu, !mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u))) {
-          ok = false;
-          break;
-        }
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u)))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256u * b;
-        for (int ks = 0; ks < ksteps; ++ks, ++it) {
-          const int s = it % kPairStages;
-          const uint32_t ph = (uint32_t)(it / kPairStages) & 1u;
-          if (__any_sync(0xffffffffu, !mbar_wait_poll(&full_bar[s], ph) || abort_flag)) {
-            ok = false;
-            break;
-          }
+        for (int ks = 0; ks < ksteps; ++ks, r.next(kPairStages)) {
+          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t so = (uint64_t)((uint32_t)(s * kPairStageBytes) >> 4);
+            const uint64_t so = (uint64_t)((uint32_t)(r.slot * kPairStageBytes) >> 4);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
               mma_bf16_pair(acc, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (ks > 0 || kb > 0) ? 1u : 0u);
-            mma_commit_pair_mc(&empty_bar[s], 0x3);
+            mma_commit_pair_mc(&empty_bar[r.slot], 0x3);
           }
           __syncwarp();
         }
@@ -593,14 +614,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       if (!mbar_wait(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
     }
-  } else if (warp == 3) {
+  } else if (warp == 2) {
     join_db(p.db, blockIdx.x, gridDim.x, lane);
   } else if (warp >= kFirstEpiWarp) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int qd = warp & 3, ch = (warp - kFirstEpiWarp) >> 2;
     const uint32_t acc_empty_even[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
     uint8_t* box = smem + (size_t)kPairStages * kPairStageBytes + (size_t)(warp - kFirstEpiWarp) * kEpiBox;
-    const int chunks = p.bn / 128;                 // 64-column chunks of this warp
+    const int chunks = (half + 63) / 64;           // 64-column chunks of this warp, the last may be narrower
     int tc = 0;
     PairTile t;
     for (int i = 0; pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
@@ -613,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int rows = min(32, q.M - row0);        // <= 0: none of this warp's rows exist
       bool gone = false;
       for (int c = 0; c < chunks; ++c) {
-        const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(64, q.N - col0);
+        const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(min(64, half - 64 * c), q.N - col0);
         BoxLoad res;
         const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
         if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);

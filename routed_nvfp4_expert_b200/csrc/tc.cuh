@@ -139,6 +139,11 @@ RNX_DEVICE void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uin
       : "memory");
 }
 
+// Ask L2 for the box at (x, y); no completion to wait for.
+RNX_DEVICE void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 // 2D tiled store of the box at (x, y) from shared memory (the layout the
 // tensor map's swizzle describes), tracked by the thread's bulk async-group.
 // Rows or columns outside the tensor are not written.
