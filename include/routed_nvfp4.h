@@ -466,9 +466,10 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, cons
  *   d_weights   fp32 [T, k], NULL = no such term
  *   counts      int32 [num_seqs, E] of moe_balance_loss, d_loss fp32
  *               [num_seqs]; both NULL = no balance term
- *   d_logits    out fp32 [T, E]; rows outside all sequences are left as they
- *               were
- * A zero score sum (S_t or C_t) gives zero for its term. At least one of
+ *   d_logits    out fp32 [T, E], not overlapping the inputs; rows outside all
+ *               sequences are left as they were
+ * A zero score sum (S_t or C_t) gives zero for its term; in both calls a score
+ * below 2^-126 counts as 0. At least one of
  * d_weights and d_loss is required. Needs no workspace.
  */
 moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,

@@ -26,18 +26,27 @@ namespace {
 constexpr int kSumWarps = 32;          // forward: one 1024-thread CTA per SM, one row per warp
 constexpr int kGradWarps = 8;
 
-// sigmoid(l) and sigmoid(l) (1 - sigmoid(l)) from e = exp(-|l|) <= 1: neither
-// form subtracts, so both keep their relative accuracy in the tails.
-RNX_DEVICE void score_of(float l, float& s, float& ds) {
-  const float e = expf(-fabsf(l));
-  const float r = __fdividef(1.0f, 1.0f + e);       // 1 + e in [1, 2]
-  s = l >= 0.f ? r : e * r;
-  ds = e * r * r;
+// e = exp(-|l|) <= 1 and r = 1 / (1 + e) = sigmoid(|l|): then sigmoid(l) is r
+// or e r, and sigmoid(l) (1 - sigmoid(l)) = e r r, none with a subtraction, so
+// all keep their relative accuracy in the tails. The exponential is 2^(l log2 e)
+// with the product's rounding error put back to first order, the two function
+// units' approximations are within 2^-22, and a score below 2^-126 is 0: at a
+// few instructions per logit the sums stay behind the memory (expf and a full
+// division were 2.5 times the HBM time at 131072 x 288).
+RNX_DEVICE void exp_parts(float l, float& e, float& r) {
+  const float x = fabsf(l);
+  const float t = -1.4426950408889634f * x;
+  const float lost = fmaf(-1.4426950408889634f, x, -t);
+  float p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+  e = fmaf(p * 0.6931471805599453f, lost, p);
+  e = x > 126.f ? 0.f : e;                     // an infinity's lost part is NaN
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
 }
 
 RNX_DEVICE float score_of(float l) {
-  const float e = expf(-fabsf(l));
-  const float r = __fdividef(1.0f, 1.0f + e);
+  float e, r;
+  exp_parts(l, e, r);
   return l >= 0.f ? r : e * r;
 }
 
@@ -89,7 +98,7 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
     load(row + kSumWarps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = lane + 32 * i < E ? score_of(s[i]) : 0.f;
+      s[i] = score_of(s[i]);                               // 0 behind the last expert
       total += s[i];
     }
     total = warp_sum(total);
@@ -243,11 +252,18 @@ struct GradParams {
 };
 
 // One warp per row, each warp a run of consecutive rows (so that the loads f
-// of its sequence stay in registers).
+// of its sequence stay in registers); the next row's logits are in flight
+// meanwhile. The routing weights' part of a row, k values, is spread over the
+// experts through a zeroed row in shared memory (testing each expert against
+// k ids cost more instructions than everything else).
 template <int NV>
 __global__ void __launch_bounds__(kGradWarps * 32) router_grad_kernel(const GradParams p) {
+  extern __shared__ float spread[];                // [kGradWarps, E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.E, k = p.k;
+  float* mine = spread + warp * E;
+  for (int e = lane; e < E; e += 32) mine[e] = 0.f;
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
   const long long first = ((long long)blockIdx.x * kGradWarps + warp) * p.rows_per_warp;
@@ -257,7 +273,19 @@ __global__ void __launch_bounds__(kGradWarps * 32) router_grad_kernel(const Grad
   if (b >= p.B) return;
   int start = seq_start(p.off, b, p.T), end = seq_start(p.off, b + 1, p.T);
   bool fresh = true;
-  float f[NV], gain = 0.f;
+  float f[NV], next[NV], gain = 0.f, next_v = 0.f;
+  int next_id = -1;
+  auto load = [&](int row) {
+    if (row >= r1) return;
+    const float* src = p.logits + (size_t)row * E + lane;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) next[i] = lane + 32 * i < E ? src[32 * i] : -INFINITY;
+    if (lane < k && p.d_weights) {
+      next_id = p.ids[(size_t)row * k + lane];
+      next_v = p.d_weights[(size_t)row * k + lane];
+    }
+  };
+  load(r0);
   for (int row = r0; row < r1; ++row) {
     while (row >= end) {                       // the next sequence that holds rows behind this one
       if (++b >= p.B) return;
@@ -265,36 +293,49 @@ __global__ void __launch_bounds__(kGradWarps * 32) router_grad_kernel(const Grad
       end = max(end, seq_start(p.off, b + 1, p.T));
       fresh = true;
     }
-    if (row < start) continue;                 // before the first sequence: left as it was
-    const float* src = p.logits + (size_t)row * E + lane;
     float l[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < E ? *(src + 32 * i) : -INFINITY;
-    int id = -1;
-    float v = 0.f;
-    if (lane < k && p.d_weights) {
-      id = *(p.ids + (size_t)row * k + lane);
-      v = *(p.d_weights + (size_t)row * k + lane);
-      if (id < 0 || id >= E) {
-        id = -1;
-        v = 0.f;
-      }
-    }
+    for (int i = 0; i < NV; ++i) l[i] = next[i];
+    const bool chosen = next_id >= 0 && next_id < E;
+    const int id = chosen ? next_id : -1;
+    const float v = chosen ? next_v : 0.f;
+    load(row + 1);
+    if (row < start) continue;                 // before the first sequence: left as it was
     if (fresh) {
       fresh = false;
       const float n = (float)(end - start);
-      gain = p.d_loss ? *(p.d_loss + b) * p.coef / n : 0.f;
+      gain = p.d_loss ? p.d_loss[b] * p.coef / n : 0.f;
       const float fs = (float)E / ((float)k * n);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        f[i] = p.d_loss && lane + 32 * i < E ? (float)*(p.counts + (size_t)b * E + lane + 32 * i) * fs : 0.f;
+        f[i] = p.d_loss && lane + 32 * i < E ? (float)p.counts[(size_t)b * E + lane + 32 * i] * fs : 0.f;
+    }
+    if (p.d_weights) {
+      // a chosen score again from its logit (the row is in L1)
+      const float sc = id >= 0 ? score_of(p.logits[(size_t)row * E + id]) : 0.f;
+      const float c = warp_sum(sc);
+      const float ic = c == 0.f ? 0.f : 1.0f / c;
+      const float m = warp_sum(v * sc) * ic;
+      const float d = p.rsf * ic * (v - m);
+      // an expert named in several slots gets their sum, in slot order, from its first
+      float sum = 0.f;
+      bool lead = id >= 0;
+      for (int j = 0; j < k; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, id, j);
+        const float dj = __shfl_sync(0xffffffffu, d, j);
+        sum += ej == id ? dj : 0.f;
+        lead = lead && !(ej == id && j < lane);
+      }
+      if (lead) mine[id] = sum;
+      __syncwarp();
     }
     float ds[NV], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float s;
-      score_of(l[i], s, ds[i]);
-      if (lane + 32 * i >= E) s = ds[i] = 0.f;
+      float e, r;
+      exp_parts(l[i], e, r);
+      const float s = l[i] >= 0.f ? r : e * r;
+      ds[i] = e * r * r;
       total += s;
       dot = fmaf(f[i], s, dot);
     }
@@ -302,40 +343,36 @@ __global__ void __launch_bounds__(kGradWarps * 32) router_grad_kernel(const Grad
     dot = warp_sum(dot);
     const float inv = total == 0.f ? 0.f : 1.0f / total;
     const float mean = dot * inv, scale = gain * inv;
-    float g[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) g[i] = scale * (f[i] - mean);
-    if (p.d_weights) {
-      // the chosen scores again from their logits (the row is in L1 / L2)
-      const float sc = id >= 0 ? score_of(*(p.logits + (size_t)row * E + id)) : 0.f;
-      const float c = warp_sum(sc);
-      const float ic = c == 0.f ? 0.f : 1.0f / c;
-      const float m = warp_sum(v * sc) * ic;
-      const float d = p.rsf * ic * (v - m);
-      for (int j = 0; j < k; ++j) {            // slot order: an expert named twice gets both parts
-        const int ej = __shfl_sync(0xffffffffu, id, j);
-        const float dj = __shfl_sync(0xffffffffu, d, j);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) g[i] += ej == lane + 32 * i ? dj : 0.f;   // a dropped slot has id -1
-      }
-    }
     float* dst = p.d_logits + (size_t)row * E + lane;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (lane + 32 * i < E) dst[32 * i] = g[i] * ds[i];
+      if (lane + 32 * i < E) dst[32 * i] = (scale * (f[i] - mean) + mine[lane + 32 * i]) * ds[i];
+    if (p.d_weights) {
+      __syncwarp();
+      if (id >= 0) mine[id] = 0.f;
+      __syncwarp();
+    }
   }
 }
 
 // Registers per lane for a row: the smallest instantiated count that holds E.
-#define RNX_BY_ROW(E, CALL)       \
-  do {                            \
-    const int nv_ = ((E) + 31) / 32; \
-    if (nv_ <= 2) CALL(2);        \
-    else if (nv_ <= 4) CALL(4);   \
-    else if (nv_ <= 8) CALL(8);   \
-    else if (nv_ <= 12) CALL(12); \
-    else if (nv_ <= 16) CALL(16); \
-    else CALL(32);                \
+#define RNX_BY_ROW(E, CALL)          \
+  do {                               \
+    switch (((E) + 31) / 32) {       \
+      case 1: CALL(1); break;        \
+      case 2: CALL(2); break;        \
+      case 3: CALL(3); break;        \
+      case 4: CALL(4); break;        \
+      case 5: CALL(5); break;        \
+      case 6: CALL(6); break;        \
+      case 7: CALL(7); break;        \
+      case 8: CALL(8); break;        \
+      case 9: CALL(9); break;        \
+      case 10: CALL(10); break;      \
+      case 11: case 12: CALL(12); break;                     \
+      case 13: case 14: case 15: case 16: CALL(16); break;   \
+      default: CALL(32); break;      \
+    }                                \
   } while (0)
 
 }  // namespace
@@ -386,12 +423,14 @@ cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, i
                                float rsf, const int32_t* off, int B, float coef, const int32_t* counts,
                                const float* d_loss, float* d_logits, cudaStream_t st) {
   GradParams p{logits, ids, d_weights, off, counts, d_loss, d_logits, T, E, k, B, 1, coef, rsf};
-  // up to 32 resident warps per SM; beyond that each warp takes a run of rows
-  p.rows_per_warp = max(1, (T + kNumSMs * 32 - 1) / (kNumSMs * 32));
+  // one wave: 32 resident warps per SM at 64 registers (E <= 288), 24 above;
+  // beyond that each warp takes a run of rows
+  const int warps = kNumSMs * (E <= 288 ? 32 : 24);
+  p.rows_per_warp = max(1, (T + warps - 1) / warps);
   const int rows_per_cta = kGradWarps * p.rows_per_warp;
   const int blocks = (T + rows_per_cta - 1) / rows_per_cta;
   cudaError_t err = cudaSuccess;
-#define CALL(NV) err = launch_pdl(router_grad_kernel<NV>, dim3(blocks), dim3(kGradWarps * 32), 0, st, p)
+#define CALL(NV) err = launch_pdl(router_grad_kernel<NV>, dim3(blocks), dim3(kGradWarps * 32), (size_t)kGradWarps * E * 4, st, p)
   RNX_BY_ROW(E, CALL);
 #undef CALL
   return err;
