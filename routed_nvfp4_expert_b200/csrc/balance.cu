@@ -12,9 +12,13 @@
 //   d s_(id_j) += rsf / C (v_j - sum_i v_i s_i / C)
 // and d l = d s * s (1 - s).
 //
-// Both directions are streams over the logits [T, E]: one warp owns a row in
-// registers, so its sums are warp shuffles and every logit is read once. HBM
-// bounds long inputs (4 T E bytes forward, 8 T E backward).
+// Both directions are streams over the logits [T, E] (4 T E bytes forward, 8 T
+// E backward). A row is held in registers by G lanes (8 up to E = 320), four
+// consecutive logits each, so a warp works on 32 / G rows at a time and the
+// row's sums cost 3 shuffles for four rows: with a whole warp per row the
+// shuffles, the slot loop and the bookkeeping of each row took as many issue
+// slots as its 288 logits (42 us forward at 131072 x 288, 46 us backward at
+// 65536 x 288).
 
 #include "common.cuh"
 #include "kernels.h"
@@ -23,32 +27,25 @@ namespace rnx {
 
 namespace {
 
-constexpr int kSumWarps = 32;          // forward: one 1024-thread CTA per SM, one row per warp
+constexpr int kMaxK = 16;
+constexpr int kSumWarps = 16;          // forward: one 512-thread CTA per SM
 constexpr int kGradWarps = 8;
+constexpr int kJoinWarps = 32;
 
-// e = exp(-|l|) <= 1 and r = 1 / (1 + e) = sigmoid(|l|): then sigmoid(l) is r
-// or e r, and sigmoid(l) (1 - sigmoid(l)) = e r r, none with a subtraction, so
-// all keep their relative accuracy in the tails. The exponential is 2^(l log2 e)
-// with the product's rounding error put back to first order, the two function
-// units' approximations are within 2^-22, and a score below 2^-126 is 0: at a
-// few instructions per logit the sums stay behind the memory (expf and a full
-// division were 2.5 times the HBM time at 131072 x 288).
-RNX_DEVICE void exp_parts(float l, float& e, float& r) {
-  const float x = fabsf(l);
-  const float t = -1.4426950408889634f * x;
-  const float lost = fmaf(-1.4426950408889634f, x, -t);
-  float p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-  e = fmaf(p * 0.6931471805599453f, lost, p);
-  e = x > 126.f ? 0.f : e;                     // an infinity's lost part is NaN
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+// s = 1 / (1 + E) and 1 - s = E s with E = exp(-l), on the two function units'
+// approximations (within 2^-22; the product l log2 e adds |l| 2^-24 relative):
+// four instructions a score, relative accuracy in both tails, and a score
+// below 2^-126 is 0. With expf and a division the sums took 2.5 times the HBM
+// time at 131072 x 288.
+RNX_DEVICE float score_of(float l, float& E) {
+  float s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(E) : "f"(-1.4426950408889634f * l));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + E));
+  return s;
 }
 
-RNX_DEVICE float score_of(float l) {
-  float e, r;
-  exp_parts(l, e, r);
-  return l >= 0.f ? r : e * r;
-}
+// s (1 - s); the minimum puts 1 - s = 1 where E is infinite (and s is 0).
+RNX_DEVICE float slope_of(float s, float E) { return fminf(E * s, 1.f) * s; }
 
 // Start of sequence b, clamped into [0, T] so that a wrong offset never leads
 // outside the rows (offsets NULL: one sequence of T rows).
@@ -67,68 +64,146 @@ RNX_DEVICE int seq_of_row(const int32_t* off, int B, int T, int row) {
   return lo;
 }
 
-// Sums of the rows [lo, hi) by the whole CTA: normalised scores into
-// sums[0 .. E) (fixed order: rows within a warp, then the warps) and
-// assignment counts into hist[0 .. E). warp_sums: kSumWarps * E floats.
-// All threads call it; the results are published by its last barrier.
-template <int NV>
-RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, int lo,
-                         int hi, float* warp_sums, int* hist) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < E; e += kSumWarps * 32) hist[e] = 0;
-  __syncthreads();
-  float acc[NV], next[NV];
+// Sum over the G lanes of a row.
+template <int G>
+RNX_DEVICE float row_sum(float v) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) acc[i] = 0.f;
-  int next_id = -1;
-  auto load = [&](int row) {                        // the next row's loads go out before this row's arithmetic
-    if (row < hi) {
-      const float* p = logits + (size_t)row * E + lane;
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Rows reach the registers through a ring of slots in shared memory, filled by
+// cp.async DEPTH - 1 rows ahead (74 KB in flight per SM at E = 288, which
+// covers the HBM latency; a second set of registers for the next row spilled).
+// A slot is E logits rounded up to 4, then 16 ids and 16 routing-weight
+// gradients. Lane g of a row takes logits 4 (g + G q) + i; those behind the
+// last expert (in the last quad alone, 4 G (NQ - 1) < E) are masked.
+RNX_DEVICE void cp_async16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+RNX_DEVICE void cp_async4(float* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+RNX_DEVICE void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+RNX_DEVICE void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__host__ __device__ constexpr int padded(int E) { return (E + 3) / 4 * 4; }
+__host__ __device__ constexpr int slot_floats(int E) { return padded(E) + 2 * kMaxK; }
+template <int NQ>
+__host__ __device__ constexpr int ring_depth() { return NQ <= 5 ? 4 : 2; }
+
+template <int G, int NQ>
+RNX_DEVICE void fill_slot(float* slot, const float* logits, const int32_t* ids, const float* weights, int E, int k,
+                          int row, int g) {
+  const float* src = logits + (size_t)row * E;
+  if (E % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) next[i] = lane + 32 * i < E ? *(p + 32 * i) : -INFINITY;
-      next_id = lane < k ? *(ids + (size_t)row * k + lane) : -1;
+    for (int q = 0; q < NQ; ++q) {
+      const int c = 4 * (g + G * q);
+      if (q < NQ - 1 || c < E) cp_async16(slot + c, src + c);
     }
-  };
-  load(lo + warp);
-  for (int row = lo + warp; row < hi; row += kSumWarps) {
-    float s[NV], total = 0.f;
-    const int id = next_id;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = next[i];
-    load(row + kSumWarps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      s[i] = score_of(s[i]);                               // 0 behind the last expert
-      total += s[i];
-    }
-    total = warp_sum(total);
-    const float inv = total == 0.f ? 0.f : 1.0f / total;   // a row of zero scores has no shares
-#pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
-    if (id >= 0 && id < E) atomicAdd(hist + id, 1);        // integer: the order does not matter
+  } else {
+    for (int c = g; c < E; c += G) cp_async4(slot + c, src + c);
   }
+  float* tail = slot + padded(E);
+  for (int j = g; j < k; j += G) {
+    if (ids) cp_async4(tail + j, ids + (size_t)row * k + j);
+    if (weights) cp_async4(tail + kMaxK + j, weights + (size_t)row * k + j);
+  }
+}
+
+// Sums of the rows [lo, hi) by the whole CTA: normalised scores into
+// sums[0 .. E) (fixed order: rows within a lane group, then the groups of a
+// warp, then the warps) and assignment counts into hist[0 .. E). warp_sums:
+// kSumWarps * E floats. All threads call it; the results are published by its
+// last barrier.
+template <int G, int NQ>
+RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, int lo, int hi, float* rings,
+                         float* warp_sums, int* hist) {
+  constexpr int R = 32 / G, STEP = kSumWarps * R, DEPTH = ring_depth<NQ>();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane % G;
+  const int slot = slot_floats(E);
+  float* ring = rings + (size_t)(warp * R + lane / G) * DEPTH * slot;
+  for (int e = tid; e < E; e += kSumWarps * 32) hist[e] = 0;
+  int base = lo + warp * R;                              // the warp's first row (warp-uniform)
+  const int mine = lane / G;
+  // a lane group without a row left reads the last one again and adds nothing
+  auto fill = [&](int d, int first) {
+    if (first < hi) fill_slot<G, NQ>(ring + d * slot, logits, ids, nullptr, E, k, min(first + mine, hi - 1), g);
+    cp_commit();
+  };
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (lane + 32 * i < E) warp_sums[warp * E + lane + 32 * i] = acc[i];
+  for (int d = 0; d < DEPTH - 1; ++d) fill(d, base + d * STEP);
+  __syncthreads();
+  float acc[4 * NQ];
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) acc[i] = 0.f;
+  for (int at = 0; base < hi; base += STEP, at = at == DEPTH - 1 ? 0 : at + 1) {
+    __syncwarp();                                        // the slot filled now was read one row ago
+    fill(at == 0 ? DEPTH - 1 : at - 1, base + (DEPTH - 1) * STEP);
+    cp_wait<DEPTH - 1>();
+    __syncwarp();
+    const float* src = ring + at * slot;
+    float s[4 * NQ], total = 0.f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(src + 4 * (g + G * q));
+      const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float unused;
+        float x = score_of(l[i], unused);
+        if (q == NQ - 1 && 4 * (g + G * q) + i >= E) x = 0.f;
+        s[4 * q + i] = x;
+        total += x;
+      }
+    }
+    total = row_sum<G>(total);
+    const bool exists = base + mine < hi;
+    const float inv = total == 0.f || !exists ? 0.f : 1.0f / total;      // a row of zero scores has no shares
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+    for (int j = g; j < k; j += G) {
+      const int id = __float_as_int(src[padded(E) + j]);
+      if (exists && id >= 0 && id < E) atomicAdd(hist + id, 1);          // integer: the order does not matter
+    }
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) {
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    const int c = 4 * (g + G * (i / 4)) + i % 4;
+    if (lane < G && c < E) warp_sums[warp * E + c] = acc[i];
+  }
   __syncthreads();
   for (int e = tid; e < E; e += kSumWarps * 32) {
     float v = 0.f;
-#pragma unroll 8
+#pragma unroll
     for (int w = 0; w < kSumWarps; ++w) v += warp_sums[w * E + e];
-    warp_sums[e] = v;                                      // only this thread reads or writes column e
+    warp_sums[e] = v;                                    // only this thread reads or writes column e
   }
   __syncthreads();
 }
 
+// Shared memory of a summing CTA: rings, the warps' sums, the counts.
+template <int G, int NQ>
+__host__ __device__ constexpr size_t sum_ring_floats(int E) {
+  return (size_t)kSumWarps * (32 / G) * ring_depth<NQ>() * slot_floats(E);
+}
+template <int G, int NQ>
+constexpr size_t sum_smem(int E) { return 4 * (sum_ring_floats<G, NQ>(E) + ((size_t)kSumWarps + 1) * E); }
+
 // One sequence's results from its column sums and counts (published in shared
-// memory). n = T_b. red: kSumWarps floats.
+// memory). n = T_b. red: 32 floats.
 RNX_DEVICE void finish_sequence(const float* sums, const int* hist, int E, int k, int n, float coef, int32_t* counts,
                                 float* mean, float* loss, float* red) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
   const float fs = n > 0 ? (float)E / ((float)k * (float)n) : 0.f;
   float part = 0.f;
-  for (int e = tid; e < E; e += kSumWarps * 32) {
+  for (int e = tid; e < E; e += blockDim.x) {
     const float p = sums[e] * inv_n;
     counts[e] = hist[e];
     mean[e] = p;
@@ -138,7 +213,7 @@ RNX_DEVICE void finish_sequence(const float* sums, const int* hist, int E, int k
   if (lane == 0) red[warp] = part;
   __syncthreads();
   if (warp == 0) {
-    const float v = warp_sum(red[lane]);
+    const float v = warp_sum(lane < (int)blockDim.x / 32 ? red[lane] : 0.f);
     if (lane == 0) *loss = coef * v;
   }
 }
@@ -157,17 +232,17 @@ struct BalanceParams {
 };
 
 // Few tokens: one CTA per sequence does all of it, one launch.
-template <int NV>
+template <int G, int NQ>
 __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_seq_kernel(const BalanceParams p) {
-  extern __shared__ float dyn[];
-  __shared__ float red[kSumWarps];
-  float* warp_sums = dyn;
-  int* hist = reinterpret_cast<int*>(dyn + (size_t)kSumWarps * p.E);
+  extern __shared__ __align__(16) float dyn[];
+  __shared__ float red[32];
+  float* warp_sums = dyn + sum_ring_floats<G, NQ>(p.E);
+  int* hist = reinterpret_cast<int*>(warp_sums + (size_t)kSumWarps * p.E);
   const int b = blockIdx.x;
   pdl_wait();
   pdl_trigger();
   const int lo = seq_start(p.off, b, p.T), hi = max(lo, seq_start(p.off, b + 1, p.T));
-  sum_rows<NV>(p.logits, p.ids, p.E, p.k, lo, hi, warp_sums, hist);
+  sum_rows<G, NQ>(p.logits, p.ids, p.E, p.k, lo, hi, dyn, warp_sums, hist);
   finish_sequence(warp_sums, hist, p.E, p.k, hi - lo, p.coef, p.counts + (size_t)b * p.E, p.mean + (size_t)b * p.E,
                   p.loss + b, red);
 }
@@ -175,11 +250,11 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_seq_kernel(const Ba
 // Many tokens, step 1: CTA i sums rows [i R, (i + 1) R). It may meet several
 // sequences; its part of sequence b goes to slot i + b, which is its own since
 // both only grow.
-template <int NV>
+template <int G, int NQ>
 __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_partial_kernel(const BalanceParams p) {
-  extern __shared__ float dyn[];
-  float* warp_sums = dyn;
-  int* hist = reinterpret_cast<int*>(dyn + (size_t)kSumWarps * p.E);
+  extern __shared__ __align__(16) float dyn[];
+  float* warp_sums = dyn + sum_ring_floats<G, NQ>(p.E);
+  int* hist = reinterpret_cast<int*>(warp_sums + (size_t)kSumWarps * p.E);
   pdl_wait();
   pdl_trigger();
   const int r0 = (int)min((long long)blockIdx.x * p.rows_per_block, (long long)p.T);
@@ -189,7 +264,7 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_partial_kernel(cons
     if (start >= r1) break;
     const int lo = max(r0, start), hi = min(r1, seq_start(p.off, b + 1, p.T));
     if (lo >= hi) continue;
-    sum_rows<NV>(p.logits, p.ids, p.E, p.k, lo, hi, warp_sums, hist);
+    sum_rows<G, NQ>(p.logits, p.ids, p.E, p.k, lo, hi, dyn, warp_sums, hist);
     const size_t slot = (size_t)(blockIdx.x + b) * p.E;
     for (int e = threadIdx.x; e < p.E; e += kSumWarps * 32) {
       p.psum[slot + e] = warp_sums[e];
@@ -201,11 +276,11 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_partial_kernel(cons
 
 // Step 2: one CTA per sequence adds its slots in order. Warps split the slots
 // into `parts` interleaved runs per group of 32 experts.
-__global__ void __launch_bounds__(kSumWarps * 32, 1) balance_join_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) balance_join_kernel(const BalanceParams p) {
   extern __shared__ float dyn[];
-  __shared__ float red[kSumWarps];
+  __shared__ float red[32];
   const int E = p.E, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int groups = (E + 31) / 32, parts = kSumWarps / groups;   // E <= 1024: at least one part
+  const int groups = (E + 31) / 32, parts = kJoinWarps / groups;   // E <= 1024: at least one part
   float* sums = dyn;                                              // [parts, E]
   int* hist = reinterpret_cast<int*>(dyn + (size_t)parts * E);    // [parts, E]
   const int b = blockIdx.x;
@@ -228,7 +303,7 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_join_kernel(const B
     hist[part * E + e] = c;
   }
   __syncthreads();
-  for (int x = tid; x < E; x += kSumWarps * 32) {
+  for (int x = tid; x < E; x += kJoinWarps * 32) {
     for (int q = 1; q < parts; ++q) {
       sums[x] += sums[q * E + x];
       hist[x] += hist[q * E + x];
@@ -251,134 +326,218 @@ struct GradParams {
   float coef, rsf;
 };
 
-// One warp per row, each warp a run of consecutive rows (so that the loads f
-// of its sequence stay in registers); the next row's logits are in flight
-// meanwhile. The routing weights' part of a row, k values, is spread over the
-// experts through a zeroed row in shared memory (testing each expert against
-// k ids cost more instructions than everything else).
-template <int NV>
-__global__ void __launch_bounds__(kGradWarps * 32) router_grad_kernel(const GradParams p) {
-  extern __shared__ float spread[];                // [kGradWarps, E]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = p.E, k = p.k;
-  float* mine = spread + warp * E;
-  for (int e = lane; e < E; e += 32) mine[e] = 0.f;
-  __syncwarp();
+// G lanes per row, each warp a run of consecutive rows, so that the loads f of
+// its sequence stay in registers. The routing weights' part of a row, k values,
+// is spread over the experts through the row's own slot, read and zeroed by
+// then (testing each expert against k ids cost more instructions than
+// everything else).
+template <int G, int NQ>
+__global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const GradParams p) {
+  constexpr int R = 32 / G, DEPTH = ring_depth<NQ>();
+  extern __shared__ __align__(16) float dyn[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G;
+  const int E = p.E, k = p.k, slot = slot_floats(p.E), tail = padded(p.E);
+  const bool vec = E % 4 == 0;
+  float* ring = dyn + (size_t)(warp * R + lane / G) * DEPTH * slot;
   pdl_wait();
   pdl_trigger();
   const long long first = ((long long)blockIdx.x * kGradWarps + warp) * p.rows_per_warp;
   if (first >= p.T) return;
   const int r0 = (int)first, r1 = (int)min(first + p.rows_per_warp, (long long)p.T);
-  int b = seq_of_row(p.off, p.B, p.T, r0);
-  if (b >= p.B) return;
-  int start = seq_start(p.off, b, p.T), end = seq_start(p.off, b + 1, p.T);
-  bool fresh = true;
-  float f[NV], next[NV], gain = 0.f, next_v = 0.f;
-  int next_id = -1;
-  auto load = [&](int row) {
-    if (row >= r1) return;
-    const float* src = p.logits + (size_t)row * E + lane;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) next[i] = lane + 32 * i < E ? src[32 * i] : -INFINITY;
-    if (lane < k && p.d_weights) {
-      next_id = p.ids[(size_t)row * k + lane];
-      next_v = p.d_weights[(size_t)row * k + lane];
-    }
+  const int32_t* ids = p.d_weights ? p.ids : nullptr;
+  int base = r0;                                 // the warp's first row (warp-uniform)
+  const int mine = lane / G;
+  auto fill = [&](int d, int from) {
+    if (from < r1) fill_slot<G, NQ>(ring + d * slot, p.logits, ids, p.d_weights, E, k, min(from + mine, r1 - 1), g);
+    cp_commit();
   };
-  load(r0);
-  for (int row = r0; row < r1; ++row) {
-    while (row >= end) {                       // the next sequence that holds rows behind this one
-      if (++b >= p.B) return;
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) fill(d, base + d * R);
+  // this lane group's sequence [start, end); the groups of a warp may be in different ones
+  int b = seq_of_row(p.off, p.B, p.T, min(base + mine, p.T - 1));
+  int start = b < p.B ? seq_start(p.off, b, p.T) : p.T, end = b < p.B ? seq_start(p.off, b + 1, p.T) : p.T;
+  bool fresh = true;
+  float f[4 * NQ], gain = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) f[i] = 0.f;
+  for (int at = 0; base < r1; base += R, at = at == DEPTH - 1 ? 0 : at + 1) {
+    __syncwarp();                                // the slot filled now was read one row ago
+    fill(at == 0 ? DEPTH - 1 : at - 1, base + (DEPTH - 1) * R);
+    const int row = base + mine;
+    while (b < p.B && row >= end) {              // the next sequence that holds rows behind this one
+      ++b;
       start = end;
-      end = max(end, seq_start(p.off, b + 1, p.T));
+      if (b < p.B) end = max(end, seq_start(p.off, b + 1, p.T));
       fresh = true;
     }
-    float l[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = next[i];
-    const bool chosen = next_id >= 0 && next_id < E;
-    const int id = chosen ? next_id : -1;
-    const float v = chosen ? next_v : 0.f;
-    load(row + 1);
-    if (row < start) continue;                 // before the first sequence: left as it was
-    if (fresh) {
+    const bool inside = row < r1 && b < p.B && row >= start;   // others are left as they were
+    if (inside && fresh && p.d_loss) {
       fresh = false;
       const float n = (float)(end - start);
-      gain = p.d_loss ? p.d_loss[b] * p.coef / n : 0.f;
+      gain = p.d_loss[b] * p.coef / n;
       const float fs = (float)E / ((float)k * n);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        f[i] = p.d_loss && lane + 32 * i < E ? (float)p.counts[(size_t)b * E + lane + 32 * i] * fs : 0.f;
+      for (int i = 0; i < 4 * NQ; ++i) {
+        const int c = 4 * (g + G * (i / 4)) + i % 4;
+        f[i] = c < E ? (float)p.counts[(size_t)b * E + c] * fs : 0.f;
+      }
+    }
+    cp_wait<DEPTH - 1>();
+    __syncwarp();
+    float* src = ring + at * slot;
+    int id[2] = {-1, -1};                        // G >= 8 lanes cover 16 slots in two
+    float d[2];
+    if (p.d_weights) {
+      float sc[2] = {0.f, 0.f}, v[2] = {0.f, 0.f}, unused;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at_j = g + G * j;
+        if (!inside || at_j >= k) continue;
+        const int e = __float_as_int(src[tail + at_j]);
+        if (e < 0 || e >= E) continue;
+        id[j] = e;
+        v[j] = src[tail + kMaxK + at_j];
+        sc[j] = score_of(src[e], unused);
+      }
+      const float c = row_sum<G>(sc[0] + sc[1]);
+      const float ic = c == 0.f ? 0.f : 1.0f / c;
+      const float m = row_sum<G>(v[0] * sc[0] + v[1] * sc[1]) * ic;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) d[j] = p.rsf * ic * (v[j] - m);
+    }
+    float l[4 * NQ], total = 0.f, dot = 0.f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float4* cell = reinterpret_cast<float4*>(src + 4 * (g + G * q));
+      const float4 v = *cell;
+      l[4 * q] = v.x, l[4 * q + 1] = v.y, l[4 * q + 2] = v.z, l[4 * q + 3] = v.w;
     }
     if (p.d_weights) {
-      // a chosen score again from its logit (the row is in L1)
-      const float sc = id >= 0 ? score_of(p.logits[(size_t)row * E + id]) : 0.f;
-      const float c = warp_sum(sc);
-      const float ic = c == 0.f ? 0.f : 1.0f / c;
-      const float m = warp_sum(v * sc) * ic;
-      const float d = p.rsf * ic * (v - m);
-      // an expert named in several slots gets their sum, in slot order, from its first
-      float sum = 0.f;
-      bool lead = id >= 0;
-      for (int j = 0; j < k; ++j) {
-        const int ej = __shfl_sync(0xffffffffu, id, j);
-        const float dj = __shfl_sync(0xffffffffu, d, j);
-        sum += ej == id ? dj : 0.f;
-        lead = lead && !(ej == id && j < lane);
-      }
-      if (lead) mine[id] = sum;
-      __syncwarp();
-    }
-    float ds[NV], total = 0.f, dot = 0.f;
+      __syncwarp();                              // the chosen logits have been read
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e, r;
-      exp_parts(l[i], e, r);
-      const float s = l[i] >= 0.f ? r : e * r;
-      ds[i] = e * r * r;
+      for (int q = 0; q < NQ; ++q) {
+        const int c = 4 * (g + G * q);
+        if (q < NQ - 1 || c < E) *reinterpret_cast<float4*>(src + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      // an expert named in several slots gets their sum, in slot order, from its first
+      float sum[2] = {0.f, 0.f};
+      bool lead[2] = {id[0] >= 0, id[1] >= 0};
+      for (int j = 0; j < k; ++j) {
+        const int other = j < G ? id[0] : id[1];
+        const float od = j < G ? d[0] : d[1];
+        const int ej = __shfl_sync(0xffffffffu, other, j % G, G);
+        const float dj = __shfl_sync(0xffffffffu, od, j % G, G);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sum[h] += ej == id[h] ? dj : 0.f;
+          lead[h] = lead[h] && !(ej == id[h] && j < g + G * h);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lead[h]) src[id[h]] = sum[h];
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) {
+      float ex, s = score_of(l[i], ex);
+      if (i >= 4 * NQ - 4 && 4 * (g + G * (NQ - 1)) + i % 4 >= E) s = 0.f;
+      l[i] = slope_of(s, ex);
       total += s;
       dot = fmaf(f[i], s, dot);
     }
-    total = warp_sum(total);
-    dot = warp_sum(dot);
+    total = row_sum<G>(total);
+    dot = row_sum<G>(dot);
     const float inv = total == 0.f ? 0.f : 1.0f / total;
     const float mean = dot * inv, scale = gain * inv;
-    float* dst = p.d_logits + (size_t)row * E + lane;
+    __syncwarp();                                // the spread row is complete
+    if (inside) {
+      float* dst = p.d_logits + (size_t)row * E;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane + 32 * i < E) dst[32 * i] = (scale * (f[i] - mean) + mine[lane + 32 * i]) * ds[i];
-    if (p.d_weights) {
-      __syncwarp();
-      if (id >= 0) mine[id] = 0.f;
-      __syncwarp();
+      for (int q = 0; q < NQ; ++q) {
+        const int c = 4 * (g + G * q);
+        if (q == NQ - 1 && c >= E) break;
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.d_weights) w = *reinterpret_cast<const float4*>(src + c);
+        const float4 o = make_float4(fmaf(scale, f[4 * q] - mean, w.x) * l[4 * q],
+                                     fmaf(scale, f[4 * q + 1] - mean, w.y) * l[4 * q + 1],
+                                     fmaf(scale, f[4 * q + 2] - mean, w.z) * l[4 * q + 2],
+                                     fmaf(scale, f[4 * q + 3] - mean, w.w) * l[4 * q + 3]);
+        if (vec) {
+          *reinterpret_cast<float4*>(dst + c) = o;
+        } else {
+          dst[c] = o.x;
+          if (q < NQ - 1 || c + 1 < E) dst[c + 1] = o.y;
+          if (q < NQ - 1 || c + 2 < E) dst[c + 2] = o.z;
+          if (q < NQ - 1 || c + 3 < E) dst[c + 3] = o.w;
+        }
+      }
     }
   }
+  cp_wait<0>();
 }
 
-// Registers per lane for a row: the smallest instantiated count that holds E.
-#define RNX_BY_ROW(E, CALL)          \
-  do {                               \
-    switch (((E) + 31) / 32) {       \
-      case 1: CALL(1); break;        \
-      case 2: CALL(2); break;        \
-      case 3: CALL(3); break;        \
-      case 4: CALL(4); break;        \
-      case 5: CALL(5); break;        \
-      case 6: CALL(6); break;        \
-      case 7: CALL(7); break;        \
-      case 8: CALL(8); break;        \
-      case 9: CALL(9); break;        \
-      case 10: CALL(10); break;      \
-      case 11: case 12: CALL(12); break;                     \
-      case 13: case 14: case 15: case 16: CALL(16); break;   \
-      default: CALL(32); break;      \
-    }                                \
+// Lanes per row and quads per lane for E <= 1024 experts: at most 10 quads (40
+// registers a row) up to 640.
+#define RNX_BY_ROW(E, CALL)                                      \
+  do {                                                           \
+    if ((E) <= 320) {                                            \
+      switch (((E) + 31) / 32) {                                 \
+        case 1: CALL(8, 1); break;                               \
+        case 2: CALL(8, 2); break;                               \
+        case 3: CALL(8, 3); break;                               \
+        case 4: CALL(8, 4); break;                               \
+        case 5: CALL(8, 5); break;                               \
+        case 6: CALL(8, 6); break;                               \
+        case 7: CALL(8, 7); break;                               \
+        case 8: CALL(8, 8); break;                               \
+        case 9: CALL(8, 9); break;                               \
+        default: CALL(8, 10); break;                             \
+      }                                                          \
+    } else if ((E) <= 640) {                                     \
+      switch (((E) + 63) / 64) {                                 \
+        case 6: CALL(16, 6); break;                              \
+        case 7: CALL(16, 7); break;                              \
+        case 8: CALL(16, 8); break;                              \
+        case 9: CALL(16, 9); break;                              \
+        default: CALL(16, 10); break;                            \
+      }                                                          \
+    } else {                                                     \
+      switch (((E) + 127) / 128) {                               \
+        case 6: CALL(32, 6); break;                              \
+        case 7: CALL(32, 7); break;                              \
+        default: CALL(32, 8); break;                             \
+      }                                                          \
+    }                                                            \
   } while (0)
+
+template <int G, int NQ>
+cudaError_t launch_sums(const BalanceParams& p, int blocks, cudaStream_t st) {
+  static std::atomic<uint64_t> done[2];
+  static_assert(sum_smem<G, NQ>(4 * G * NQ) <= kMaxDynamicSmem, "shared memory");
+  const size_t smem = sum_smem<G, NQ>(p.E);
+  auto kern = blocks ? balance_partial_kernel<G, NQ> : balance_seq_kernel<G, NQ>;
+  const cudaError_t e = smem > 48 * 1024 ? allow_smem(kern, done[blocks > 0]) : cudaSuccess;
+  return e != cudaSuccess ? e : launch_pdl(kern, dim3(blocks ? blocks : p.B), dim3(kSumWarps * 32), smem, st, p);
+}
+
+template <int G, int NQ>
+cudaError_t launch_grad(GradParams p, cudaStream_t st) {
+  constexpr int R = 32 / G;
+  // one wave of 16 warps per SM; beyond that each warp takes a run of rows
+  const int groups = (p.T + R - 1) / R, warps = kNumSMs * 2 * kGradWarps;
+  p.rows_per_warp = R * max(1, (groups + warps - 1) / warps);
+  const int rows = kGradWarps * p.rows_per_warp;
+  const size_t smem = (size_t)kGradWarps * R * ring_depth<NQ>() * slot_floats(p.E) * 4;   // at most 100 KB
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = smem > 48 * 1024 ? allow_smem(router_grad_kernel<G, NQ>, done) : cudaSuccess;
+  return e != cudaSuccess ? e : launch_pdl(router_grad_kernel<G, NQ>, dim3((p.T + rows - 1) / rows), dim3(kGradWarps * 32), smem, st, p);
+}
 
 }  // namespace
 
 int balance_rows_per_block(int T) {
-  return max(kSumWarps, (T + kNumSMs - 1) / kNumSMs);      // one CTA per SM
+  return max(64, (T + kNumSMs - 1) / kNumSMs);      // one CTA per SM
 }
 
 int balance_blocks(int T) {
@@ -390,47 +549,25 @@ int balance_blocks(int T) {
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
                                 cudaStream_t st) {
-  BalanceParams p{logits, ids, off, T, E, k, B, balance_rows_per_block(T), coef, nullptr, nullptr, counts, mean, loss};
-  const size_t smem = ((size_t)kSumWarps + 1) * E * 4;
   const int blocks = balance_blocks(T);
+  float* psum = static_cast<float*>(scratch);
+  BalanceParams p{logits, ids, off, T, E, k, B, balance_rows_per_block(T), coef, psum,
+                  reinterpret_cast<int*>(psum + (size_t)(blocks + B) * E), counts, mean, loss};
   cudaError_t err = cudaSuccess;
-  if (blocks == 0) {
-#define CALL(NV)                                                                                                  \
-  do {                                                                                                            \
-    if (smem > 48 * 1024) err = cudaFuncSetAttribute(balance_seq_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
-    if (err == cudaSuccess) err = launch_pdl(balance_seq_kernel<NV>, dim3(B), dim3(kSumWarps * 32), smem, st, p);        \
-  } while (0)
-    RNX_BY_ROW(E, CALL);
-#undef CALL
-    return err;
-  }
-  p.psum = static_cast<float*>(scratch);
-  p.pcnt = reinterpret_cast<int*>(p.psum + (size_t)(blocks + B) * E);
-#define CALL(NV)                                                                                                  \
-  do {                                                                                                            \
-    if (smem > 48 * 1024) err = cudaFuncSetAttribute(balance_partial_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
-    if (err == cudaSuccess) err = launch_pdl(balance_partial_kernel<NV>, dim3(blocks), dim3(kSumWarps * 32), smem, st, p); \
-  } while (0)
+#define CALL(G, NQ) err = launch_sums<G, NQ>(p, blocks, st)
   RNX_BY_ROW(E, CALL);
 #undef CALL
-  if (err != cudaSuccess) return err;
-  // [parts, E] twice: parts * E <= kSumWarps * 32 + E at most
-  const int parts = kSumWarps / ((E + 31) / 32);
-  return launch_pdl(balance_join_kernel, dim3(B), dim3(kSumWarps * 32), (size_t)parts * E * 8, st, p);
+  if (err != cudaSuccess || blocks == 0) return err;
+  const int parts = kJoinWarps / ((E + 31) / 32);
+  return launch_pdl(balance_join_kernel, dim3(B), dim3(kJoinWarps * 32), (size_t)parts * E * 8, st, p);
 }
 
 cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, int E, int k, const float* d_weights,
                                float rsf, const int32_t* off, int B, float coef, const int32_t* counts,
                                const float* d_loss, float* d_logits, cudaStream_t st) {
-  GradParams p{logits, ids, d_weights, off, counts, d_loss, d_logits, T, E, k, B, 1, coef, rsf};
-  // one wave: 32 resident warps per SM at 64 registers (E <= 288), 24 above;
-  // beyond that each warp takes a run of rows
-  const int warps = kNumSMs * (E <= 288 ? 32 : 24);
-  p.rows_per_warp = max(1, (T + warps - 1) / warps);
-  const int rows_per_cta = kGradWarps * p.rows_per_warp;
-  const int blocks = (T + rows_per_cta - 1) / rows_per_cta;
+  const GradParams p{logits, ids, d_weights, off, counts, d_loss, d_logits, T, E, k, B, 1, coef, rsf};
   cudaError_t err = cudaSuccess;
-#define CALL(NV) err = launch_pdl(router_grad_kernel<NV>, dim3(blocks), dim3(kGradWarps * 32), (size_t)kGradWarps * E * 4, st, p)
+#define CALL(G, NQ) err = launch_grad<G, NQ>(p, st)
   RNX_BY_ROW(E, CALL);
 #undef CALL
   return err;

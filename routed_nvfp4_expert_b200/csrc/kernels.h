@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "../../include/routed_nvfp4.h"
@@ -61,6 +62,21 @@ template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {
   return launch_ex(kern, grid, block, smem, st, true, launch_priority_high(), std::forward<Args>(args)...);
+}
+
+// Opt-in shared memory of a kernel, set once per device (`done`: a static of
+// the call site, one bit per device).
+constexpr int kMaxDynamicSmem = 226 * 1024;   // the limit of 227 KB less the kernels' static barriers
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 struct ExpertGemvArgs {
@@ -310,8 +326,6 @@ cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, i
                                const float* d_loss, float* d_logits, cudaStream_t st);
 
 // ---------------------------------------------------------------- BF16 linear layer (linear.cu)
-
-constexpr int kLinearMaxSmem = 226 * 1024;   // opt-in limit of 227 KB less the kernels' static barriers
 
 // Workspace offsets: the status word, then what the call needs of copies of x
 // and w in 16-byte-aligned rows, dz and the partial column sums of db.

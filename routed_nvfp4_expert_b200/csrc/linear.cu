@@ -18,8 +18,6 @@
 // each element; y, z, dx and dW take the same one rounding); db is summed in
 // fp32 from the unrounded dz.
 
-#include <atomic>
-
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -367,7 +365,7 @@ constexpr int kEpiBox = 32 * 128;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kEpiBox + 1024;
 constexpr uint32_t kPairTmemCols = 512;
 constexpr int kRaster = 16;                                  // m tiles per raster group
-static_assert(kPairSmem <= kLinearMaxSmem, "shared memory");
+static_assert(kPairSmem <= kMaxDynamicSmem, "shared memory");
 
 struct PairProblem {
   CUtensorMap tma_a, tma_b;
@@ -856,19 +854,6 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
 }
 
 // ---------------------------------------------------------------- host side
-
-// Opt-in shared memory of a kernel, once per device.
-template <typename K>
-cudaError_t allow_smem(K kern, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinearMaxSmem);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
 
 // One operand of a product: `rows` x `red` elements (red = the reduction).
 // mn: memory is [red, rows] with pitch ld, else [rows, red].
