@@ -31,6 +31,10 @@ constexpr int kMaxK = 16;
 constexpr int kSumWarps = 16;          // forward: one 512-thread CTA per SM
 constexpr int kGradWarps = 8;
 constexpr int kJoinWarps = 32;
+// Up to these many tokens a whole warp takes a row: 2.8 against 3.5 us forward
+// at one token of 288 experts, 3.8 against 5.7 us backward at 1024 (one row per
+// resident warp); above, 4.2 against 4.0 us at 32 and 6.4 against 5.9 us at 3000.
+constexpr int kSumWideT = 16, kGradWideT = kNumSMs * 2 * kGradWarps;
 
 // s = 1 / (1 + E) and 1 - s = E s with E = exp(-l), on the two function units'
 // approximations (within 2^-22; the product l log2 e adds |l| 2^-24 relative):
@@ -93,6 +97,14 @@ __host__ __device__ constexpr int slot_floats(int E) { return padded(E) + 2 * kM
 template <int NQ>
 __host__ __device__ constexpr int ring_depth() { return NQ <= 5 ? 4 : 2; }
 
+// Where lane g reads its quad q of a slot: the last quad's lanes behind the
+// last expert read the row's last four again, so that no read leaves the slot.
+template <int G, int NQ>
+RNX_DEVICE int cell(int q, int g, int E) {
+  const int c = 4 * (g + G * q);
+  return q == NQ - 1 ? min(c, padded(E) - 4) : c;
+}
+
 template <int G, int NQ>
 RNX_DEVICE void fill_slot(float* slot, const float* logits, const int32_t* ids, const float* weights, int E, int k,
                           int row, int g) {
@@ -148,7 +160,7 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
     float s[4 * NQ], total = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(src + 4 * (g + G * q));
+      const float4 v = *reinterpret_cast<const float4*>(src + cell<G, NQ>(q, g, E));
       const float l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -408,8 +420,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
     float l[4 * NQ], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      float4* cell = reinterpret_cast<float4*>(src + 4 * (g + G * q));
-      const float4 v = *cell;
+      const float4 v = *reinterpret_cast<const float4*>(src + cell<G, NQ>(q, g, E));
       l[4 * q] = v.x, l[4 * q + 1] = v.y, l[4 * q + 2] = v.z, l[4 * q + 3] = v.w;
     }
     if (p.d_weights) {
@@ -478,35 +489,42 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
 }
 
 // Lanes per row and quads per lane for E <= 1024 experts: at most 10 quads (40
-// registers a row) up to 640.
-#define RNX_BY_ROW(E, CALL)                                      \
+// registers a row); `wide` asks for a warp per row, the shortest chain where
+// there are no more rows than warps.
+#define RNX_CASE(X, CALL, G, NQ) case X: CALL(G, NQ); break
+#define RNX_BY_ROW(E, wide, CALL)                                \
   do {                                                           \
-    if ((E) <= 320) {                                            \
-      switch (((E) + 31) / 32) {                                 \
-        case 1: CALL(8, 1); break;                               \
-        case 2: CALL(8, 2); break;                               \
-        case 3: CALL(8, 3); break;                               \
-        case 4: CALL(8, 4); break;                               \
-        case 5: CALL(8, 5); break;                               \
-        case 6: CALL(8, 6); break;                               \
-        case 7: CALL(8, 7); break;                               \
-        case 8: CALL(8, 8); break;                               \
-        case 9: CALL(8, 9); break;                               \
-        default: CALL(8, 10); break;                             \
+    if ((wide) || (E) > 640) {                                   \
+      switch (((E) + 127) / 128) {                               \
+        RNX_CASE(1, CALL, 32, 1);                                \
+        RNX_CASE(2, CALL, 32, 2);                                \
+        RNX_CASE(3, CALL, 32, 3);                                \
+        RNX_CASE(4, CALL, 32, 4);                                \
+        RNX_CASE(5, CALL, 32, 5);                                \
+        RNX_CASE(6, CALL, 32, 6);                                \
+        RNX_CASE(7, CALL, 32, 7);                                \
+        default: CALL(32, 8);                                    \
       }                                                          \
-    } else if ((E) <= 640) {                                     \
+    } else if ((E) > 320) {                                      \
       switch (((E) + 63) / 64) {                                 \
-        case 6: CALL(16, 6); break;                              \
-        case 7: CALL(16, 7); break;                              \
-        case 8: CALL(16, 8); break;                              \
-        case 9: CALL(16, 9); break;                              \
-        default: CALL(16, 10); break;                            \
+        RNX_CASE(6, CALL, 16, 6);                                \
+        RNX_CASE(7, CALL, 16, 7);                                \
+        RNX_CASE(8, CALL, 16, 8);                                \
+        RNX_CASE(9, CALL, 16, 9);                                \
+        default: CALL(16, 10);                                   \
       }                                                          \
     } else {                                                     \
-      switch (((E) + 127) / 128) {                               \
-        case 6: CALL(32, 6); break;                              \
-        case 7: CALL(32, 7); break;                              \
-        default: CALL(32, 8); break;                             \
+      switch (((E) + 31) / 32) {                                 \
+        RNX_CASE(1, CALL, 8, 1);                                 \
+        RNX_CASE(2, CALL, 8, 2);                                 \
+        RNX_CASE(3, CALL, 8, 3);                                 \
+        RNX_CASE(4, CALL, 8, 4);                                 \
+        RNX_CASE(5, CALL, 8, 5);                                 \
+        RNX_CASE(6, CALL, 8, 6);                                 \
+        RNX_CASE(7, CALL, 8, 7);                                 \
+        RNX_CASE(8, CALL, 8, 8);                                 \
+        RNX_CASE(9, CALL, 8, 9);                                 \
+        default: CALL(8, 10);                                    \
       }                                                          \
     }                                                            \
   } while (0)
@@ -536,8 +554,9 @@ cudaError_t launch_grad(GradParams p, cudaStream_t st) {
 
 }  // namespace
 
+// One CTA per SM; at least a row per warp.
 int balance_rows_per_block(int T) {
-  return max(64, (T + kNumSMs - 1) / kNumSMs);      // one CTA per SM
+  return max(kSumWarps, (T + kNumSMs - 1) / kNumSMs);
 }
 
 int balance_blocks(int T) {
@@ -555,7 +574,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, 
                   reinterpret_cast<int*>(psum + (size_t)(blocks + B) * E), counts, mean, loss};
   cudaError_t err = cudaSuccess;
 #define CALL(G, NQ) err = launch_sums<G, NQ>(p, blocks, st)
-  RNX_BY_ROW(E, CALL);
+  RNX_BY_ROW(E, T <= kSumWideT, CALL);
 #undef CALL
   if (err != cudaSuccess || blocks == 0) return err;
   const int parts = kJoinWarps / ((E + 31) / 32);
@@ -568,7 +587,7 @@ cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, i
   const GradParams p{logits, ids, d_weights, off, counts, d_loss, d_logits, T, E, k, B, 1, coef, rsf};
   cudaError_t err = cudaSuccess;
 #define CALL(G, NQ) err = launch_grad<G, NQ>(p, st)
-  RNX_BY_ROW(E, CALL);
+  RNX_BY_ROW(E, T <= kGradWideT, CALL);
 #undef CALL
   return err;
 }

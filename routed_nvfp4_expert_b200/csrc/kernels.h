@@ -311,8 +311,9 @@ cudaError_t launch_w4a16_grouped_gemm(const W4a16GemmArgs& a, cudaStream_t st);
 // ---------------------------------------------------------------- router balance (balance.cu)
 
 // Inputs of up to this many tokens are summed by one CTA per sequence (one
-// launch); longer ones by one CTA per SM and a join.
-constexpr int kBalanceSeqMaxT = 256;
+// launch, 6.9 us at 128 x 288); longer ones by one CTA per SM and a join (7.9
+// against 10.1 us at 256).
+constexpr int kBalanceSeqMaxT = 128;
 // CTAs of the first step of launch_balance_loss (0: the one-launch form); its
 // scratch holds (blocks + B) * E floats and as many ints.
 int balance_blocks(int T);

@@ -98,9 +98,16 @@ CASES = [
     (256, 100, 5, [0, 255, 256], True, False),
     (257, 288, 8, [0, 257], False, False),
     (300, 1024, 16, [0, 1, 2, 150, 299], True, True),
+    # expert counts that end inside a row's last vectors, at each number of lanes per row
+    (20, 33, 3, None, False, False),
+    (90, 330, 5, [0, 40, 90], False, False),
+    (70, 650, 16, None, True, False),
+    (3000, 322, 4, [0, 1000, 2999], False, False),
+    (2500, 129, 4, None, False, False),
     (5000, 64, 6, [0, 34, 34, 35, 4000, 4990], True, False),
     (9001, 384, 8, None, False, False),
 ]
+GRAD_CASES = [c for c in CASES if c[0] <= 3000]
 
 
 @pytest.mark.parametrize("T,E,k,off,dropped,twice", CASES)
@@ -117,7 +124,7 @@ def test_balance_matches_the_formula(T, E, k, off, dropped, twice):
 
 
 @pytest.mark.parametrize("terms", ["both", "weights", "loss"])
-@pytest.mark.parametrize("T,E,k,off,dropped,twice", [c for c in CASES if c[0] <= 300])
+@pytest.mark.parametrize("T,E,k,off,dropped,twice", GRAD_CASES)
 def test_router_backward_matches_the_formula(T, E, k, off, dropped, twice, terms):
     logits, ids = _inputs(T, E, k, T * 3 + E, dropped, twice)
     ref_off = [0, T] if off is None else off
