@@ -356,24 +356,44 @@ def moe_unpermute_combine(cfg: SiteConfig, rows, T: int, plan: MoePlan, ids, sha
 
 # ------------------------------------------------------------------ router balance and gradients
 
-def _arg(t, name: str, dtype, shape) -> int | None:
-    """Pointer of a contiguous tensor on the current device with this dtype and shape (None passes)."""
-    if t is None:
-        return None
+# These calls are short on the GPU, so their checks are kept to a few plain
+# comparisons per tensor; what went wrong is worked out only when one fails.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_and_stream(stream):
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return dev, _raw_stream(dev)
+    return dev, _stream(stream) if dev >= 0 else None
+
+
+def _refuse(t, name: str, dtype, shape):
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    _same_device(t, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _same_device(t, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: on cuda:{t.get_device()}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name}: expected contiguous rows")
+
+
+def _arg(t, name: str, dtype, shape, dev: int) -> int | None:
+    """Pointer of a contiguous tensor on the current device with this dtype and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _ws(ws, dev: int):
+    """(pointer, bytes) of a workspace tensor."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, "ws", ws.dtype, tuple(ws.shape))
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _seqs(seq_offsets) -> int:
@@ -398,11 +418,12 @@ def moe_balance_loss(cfg: SiteConfig, logits, ids, coef: float, counts, mean_sco
     when it is None)."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
     f32, i32 = torch.float32, torch.int32
+    dev, st = _device_and_stream(stream)
     _check(lib().moe_balance_loss(
-        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E)), _arg(ids, "ids", i32, (T, k)), T,
-        _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, coef, _arg(counts, "counts", i32, (B, E)),
-        _arg(mean_scores, "mean_scores", f32, (B, E)), _arg(loss, "loss", f32, (B,)), _p(ws), ws.numel(),
-        _stream(stream)))
+        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
+        _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef, _arg(counts, "counts", i32, (B, E), dev),
+        _arg(mean_scores, "mean_scores", f32, (B, E), dev), _arg(loss, "loss", f32, (B,), dev),
+        *_ws(ws, dev), st))
 
 
 def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, coef: float = 0.0, counts=None,
@@ -411,26 +432,27 @@ def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, 
     and the balance loss (counts of moe_balance_loss and d_loss fp32 [B])."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
     f32, i32 = torch.float32, torch.int32
+    dev, st = _device_and_stream(stream)
     _check(lib().moe_router_backward(
-        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E)), _arg(ids, "ids", i32, (T, k)), T,
-        _arg(d_weights, "d_weights", f32, (T, k)), _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, coef,
-        _arg(counts, "counts", i32, (B, E)), _arg(d_loss, "d_loss", f32, (B,)),
-        _arg(d_logits, "d_logits", f32, (T, E)), _stream(stream)))
+        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
+        _arg(d_weights, "d_weights", f32, (T, k), dev), _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef,
+        _arg(counts, "counts", i32, (B, E), dev), _arg(d_loss, "d_loss", f32, (B,), dev),
+        _arg(d_logits, "d_logits", f32, (T, E), dev), st))
 
 
 # ------------------------------------------------------------------ BF16 linear layer
 
-def _rows(t, name: str, shape):
-    """(pointer, row pitch) of a bf16 matrix whose rows are contiguous."""
+def _rows(t, name: str, shape, dev: int):
+    """(pointer, row pitch) of a bf16 matrix whose rows are contiguous (None passes)."""
     if t is None:
         return None, 0
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected torch.bfloat16 {shape}, got {t.dtype} {tuple(t.shape)}")
-    _same_device(t, name)
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, torch.bfloat16, shape)
+    pitch, step = t.stride()
     rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: expected contiguous rows")
-    return t.data_ptr(), max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+    if step != 1 and cols > 1:
+        _refuse(t, name, torch.bfloat16, shape)
+    return t.data_ptr(), pitch if rows > 1 or pitch >= cols else cols
 
 
 def _activation(act: str) -> int:
@@ -441,7 +463,8 @@ def _activation(act: str) -> int:
 
 def _alloc_linear(size, x, w) -> torch.Tensor:
     (T, K), N = x.shape, w.shape[0]
-    n = size(T, K, N, _rows(x, "x", (T, K))[1], _rows(w, "w", (N, K))[1])
+    dev = x.get_device()
+    n = size(T, K, N, _rows(x, "x", (T, K), dev)[1], _rows(w, "w", (N, K), dev)[1])
     if n == 0:
         raise MoEError(1, lib().moe_last_error().decode())
     return torch.empty(n, dtype=torch.uint8, device=x.device)
@@ -461,27 +484,30 @@ def linear_bf16(x, w, y, ws, bias=None, residual=None, act: str = "none", z=None
     """y = act(x w^T + bias) + residual; z receives the pre-activation. x [T, K],
     w [N, K], bias [N], residual, z, y [T, N], all bf16; rows may be strided."""
     (T, K), N = x.shape, w.shape[0]
-    xp, ldx = _rows(x, "x", (T, K))
-    wp, ldw = _rows(w, "w", (N, K))
-    rp, ldr = _rows(residual, "residual", (T, N))
-    zp, ldz = _rows(z, "z", (T, N))
-    yp, ldy = _rows(y, "y", (T, N))
-    _check(lib().linear_bf16(_activation(act), xp, ldx, T, K, wp, ldw, N, _arg(bias, "bias", torch.bfloat16, (N,)), rp,
-                             ldr, zp, ldz, yp, ldy, _p(ws), ws.numel(), _stream(stream)))
+    dev, st = _device_and_stream(stream)
+    out = (T, N)
+    xp, ldx = _rows(x, "x", (T, K), dev)
+    wp, ldw = _rows(w, "w", (N, K), dev)
+    rp, ldr = _rows(residual, "residual", out, dev)
+    zp, ldz = _rows(z, "z", out, dev)
+    yp, ldy = _rows(y, "y", out, dev)
+    _check(lib().linear_bf16(_activation(act), xp, ldx, T, K, wp, ldw, N,
+                             _arg(bias, "bias", torch.bfloat16, (N,), dev), rp, ldr, zp, ldz, yp, ldy, *_ws(ws, dev), st))
 
 
 def linear_bf16_backward(dy, x, w, ws, z=None, act: str = "none", dx=None, dw=None, db=None, stream=None):
     """dz = dy act'(z); dx = dz w, dw = dz^T x (bf16), db = sum of dz over the
     tokens (fp32 [N]); each output may be None, not all."""
     (T, K), N = x.shape, w.shape[0]
-    dyp, lddy = _rows(dy, "dy", (T, N))
-    zp, ldz = _rows(z, "z", (T, N))
-    xp, ldx = _rows(x, "x", (T, K))
-    wp, ldw = _rows(w, "w", (N, K))
-    dxp, lddx = _rows(dx, "dx", (T, K))
-    dwp, lddw = _rows(dw, "dw", (N, K))
+    dev, st = _device_and_stream(stream)
+    dyp, lddy = _rows(dy, "dy", (T, N), dev)
+    zp, ldz = _rows(z, "z", (T, N), dev)
+    xp, ldx = _rows(x, "x", (T, K), dev)
+    wp, ldw = _rows(w, "w", (N, K), dev)
+    dxp, lddx = _rows(dx, "dx", (T, K), dev)
+    dwp, lddw = _rows(dw, "dw", (N, K), dev)
     _check(lib().linear_bf16_backward(_activation(act), dyp, lddy, zp, ldz, xp, ldx, T, K, wp, ldw, N, dxp, lddx, dwp,
-                                      lddw, _arg(db, "db", torch.float32, (N,)), _p(ws), ws.numel(), _stream(stream)))
+                                      lddw, _arg(db, "db", torch.float32, (N,), dev), *_ws(ws, dev), st))
 
 
 def moe_workspace_views(cfg: SiteConfig, T: int, path: int, ws) -> MoeViews:
