@@ -144,23 +144,32 @@ RNX_DEVICE void join_db(const DbJoin& d, int cta, int ctas, int lane) {
 // leaves it in its shared memory as fp32 [bn][128]; after a cluster barrier
 // CTA s adds the S parts of its share of the j rows in rank order (so the
 // result does not depend on timing), applies the epilogue and stores rows of
-// out[j, m], 128 consecutive features per warp.
+// out[j, m], 128 consecutive features per warp. Up to two products share a
+// launch (dx and dW of few tokens); a reduction of fewer steps than S leaves
+// the last ranks without a part of their own.
 // Warps: 0 = TMA producer, 1 = MMA issuer, 2 = TMEM allocator, 3 = db join,
 // 4-7 = TMEM readers; all eight reduce and store. Every wait is bounded; a
 // timeout sets the status word, and the CTA still meets its cluster's barriers.
 
 constexpr int kSplitThreads = 256;
 constexpr int kSplitMaxStages = 10;
+constexpr int kMaxSplit = 8;               // the portable cluster size
 
-struct SplitParams {
+struct SplitProblem {
   CUtensorMap tma_a, tma_b;
   Epilogue ep;
-  DbJoin db;
-  uint32_t* status;
   int M, J;                   // D's extents
   int ksteps;                 // 64-element steps of the whole reduction
-  int bn, stages, tmem_cols;
+  int bn, stages;
+  int mt, tiles;
   int a_mn, b_mn;
+};
+struct SplitParams {
+  SplitProblem prob[2];
+  DbJoin db;
+  uint32_t* status;
+  int tiles;                  // of all products
+  int S, tmem_cols;
   int clear;
 };
 
@@ -173,14 +182,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = gridDim.x, rank = blockIdx.x;
-  const int m0 = blockIdx.y * kTileM, j0 = blockIdx.z * p.bn;
-  const int k_lo = (int)((long long)p.ksteps * rank / S), k_hi = (int)((long long)p.ksteps * (rank + 1) / S);
-  const int stage_bytes = kABytes + p.bn * 128;
-  const int cta = (blockIdx.z * gridDim.y + blockIdx.y) * S + rank;
+  const int S = p.S, rank = (int)(blockIdx.x % (unsigned)S);
+  int tile = (int)(blockIdx.x / (unsigned)S);
+  const bool second = tile >= p.prob[0].tiles;
+  const SplitProblem& q = p.prob[second];
+  if (second) tile -= p.prob[0].tiles;
+  const int jt = tile / q.mt, m0 = (tile - jt * q.mt) * kTileM, j0 = jt * q.bn;
+  const int bn = q.bn, stages = q.stages;
+  const int parts = min(S, q.ksteps);
+  const int k_lo = rank < parts ? (int)((long long)q.ksteps * rank / parts) : 0;
+  const int k_hi = rank < parts ? (int)((long long)q.ksteps * (rank + 1) / parts) : 0;
+  const int stage_bytes = kABytes + bn * 128;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -200,29 +215,29 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   pdl_trigger();
   // the call's first launch clears the status word: its first CTA, and a wait
   // of another CTA that could set it runs out two seconds later at the earliest
-  if (p.clear && cta == 0 && threadIdx.x == 0) *p.status = 0u;
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
 
   if (warp == 0) {
     Ring r;
     int issued = 0;
     bool ok = true;
-    for (int ks = k_lo; ks < k_hi; ++ks, ++issued, r.next(p.stages)) {
+    for (int ks = k_lo; ks < k_hi; ++ks, ++issued, r.next(stages)) {
       if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
       if (elect_one()) {
         uint8_t* sA = smem + (size_t)r.slot * stage_bytes;
         uint8_t* sB = sA + kABytes;
         uint64_t* bar = &full_bar[r.slot];
         mbar_arrive_expect_tx(bar, (uint32_t)stage_bytes);
-        if (p.a_mn) {
-          tma_load_2d(sA, &p.tma_a, m0, ks * kStepK, bar);
-          tma_load_2d(sA + kMnBlock, &p.tma_a, m0 + 64, ks * kStepK, bar);
+        if (q.a_mn) {
+          tma_load_2d(sA, &q.tma_a, m0, ks * kStepK, bar);
+          tma_load_2d(sA + kMnBlock, &q.tma_a, m0 + 64, ks * kStepK, bar);
         } else {
-          tma_load_2d(sA, &p.tma_a, ks * kStepK, m0, bar);
+          tma_load_2d(sA, &q.tma_a, ks * kStepK, m0, bar);
         }
-        if (p.b_mn) {
-          for (int c = 0; c < p.bn; c += 64) tma_load_2d(sB + c * 128, &p.tma_b, j0 + c, ks * kStepK, bar);
+        if (q.b_mn) {
+          for (int c = 0; c < bn; c += 64) tma_load_2d(sB + c * 128, &q.tma_b, j0 + c, ks * kStepK, bar);
         } else {
-          tma_load_2d(sB, &p.tma_b, ks * kStepK, j0, bar);
+          tma_load_2d(sB, &q.tma_b, ks * kStepK, j0, bar);
         }
       }
       __syncwarp();
@@ -231,16 +246,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
       set_status(p.status, kDevErrTimeout);
       abort_flag = 1;
     }
-    ring_drain(full_bar, r, issued, p.stages, p.status, lane);
+    ring_drain(full_bar, r, issued, stages, p.status, lane);
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16_major(kTileM, p.bn, p.a_mn, p.b_mn);
+    const uint32_t idesc = idesc_bf16_major(kTileM, bn, q.a_mn, q.b_mn);
     const uint32_t s0 = smem_u32(smem);
-    const uint64_t dA0 = p.a_mn ? sdesc_mn_sw128(s0, kMnBlock) : sdesc_k_sw128(s0);
-    const uint64_t dB0 = p.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
-    const uint64_t stepA = p.a_mn ? 2048 >> 4 : 32 >> 4, stepB = p.b_mn ? 2048 >> 4 : 32 >> 4;   // K = 16
+    const uint64_t dA0 = q.a_mn ? sdesc_mn_sw128(s0, kMnBlock) : sdesc_k_sw128(s0);
+    const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
+    const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;   // K = 16
     Ring r;
     bool ok = true;
-    for (int ks = k_lo; ks < k_hi; ++ks, r.next(p.stages)) {
+    for (int ks = k_lo; ks < k_hi; ++ks, r.next(stages)) {
       if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {
@@ -260,23 +275,23 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     __syncwarp();
     if (!mbar_wait_poll(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
   } else if (warp == 3) {
-    join_db(p.db, cta, S * gridDim.y * gridDim.z, lane);
+    join_db(p.db, (int)blockIdx.x, (int)gridDim.x, lane);
   }
 
   // the producer and the issuer are through: every copy has landed and every
   // MMA is done, so the stages may hold the accumulator's fp32 values
   __syncthreads();
   float* part = reinterpret_cast<float*>(smem);            // [bn][128]
-  if (warp >= 4) {
+  if (warp >= 4 && rank < parts) {
     tc_fence_after();
-    const int q = warp & 3;
-    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
-    for (int c = 0; c < p.bn; c += 16) {
+    const int qd = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(qd * 32) << 16);
+    for (int c = 0; c < bn; c += 16) {
       uint32_t v[16];
       tmem_ld16(tq + c, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c + i) * kTileM + q * 32 + lane] = __uint_as_float(v[i]);
+      for (int i = 0; i < 16; ++i) part[(c + i) * kTileM + qd * 32 + lane] = __uint_as_float(v[i]);
     }
     tc_fence_before();
   }
@@ -284,50 +299,70 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   if (S > 1) cluster_sync_all();
 
   // ---------------------------------------------------------------- join and epilogue
-  const int nj = min(p.bn, p.J - j0), per = (nj + S - 1) / S;
+  // lane: four consecutive features where every row of z, residual and out
+  // starts on 8 bytes, else features lane + 32 i (2-byte accesses that fill
+  // whole sectors)
+  const Epilogue& ep = q.ep;
+  const int nj = min(bn, q.J - j0), per = (nj + S - 1) / S;
   const int j_lo = rank * per, j_hi = min(nj, j_lo + per);
-  const int m = m0 + 4 * lane;
-  const bool whole = p.ep.vec && m + 4 <= p.M;
+  const bool vec = ep.vec && m0 + kTileM <= q.M;
+  const int first = vec ? 4 * lane : lane, step = vec ? 1 : 32;
   float bias[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.ep.bias)
+  if (ep.bias)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (m + i < p.M) bias[i] = bf16_bits_to_f32(p.ep.bias[m + i]);
-  const uint32_t part_addr = smem_u32(part) + 16 * lane;
+      if (m0 + first + step * i < q.M) bias[i] = bf16_bits_to_f32(ep.bias[m0 + first + step * i]);
+  const uint32_t part_addr = smem_u32(part) + 4 * first;
+#pragma unroll 2
   for (int j = j_lo + warp; j < j_hi; j += kSplitThreads / 32) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (S == 1) {
-      const float4 f = *reinterpret_cast<const float4*>(part + (size_t)j * kTileM + 4 * lane);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    } else {
-#pragma unroll 8
-      for (int s = 0; s < S; ++s) {
-        const float4 f = ld_cluster_f4(mapa_shared(part_addr + j * kTileM * 4, (uint32_t)s));
-        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    const uint32_t at = part_addr + j * kTileM * 4;
+    const long long row = j0 + j;
+    const int m = m0 + first;
+    uint32_t res[4] = {0u, 0u, 0u, 0u};                     // the residual's latency beside the parts'
+    if (ep.residual) {
+      const uint16_t* src = ep.residual + row * ep.ldr + m;
+      if (vec) {
+        const uint2 r = *reinterpret_cast<const uint2*>(src);
+        res[0] = r.x << 16, res[1] = r.x & 0xFFFF0000u, res[2] = r.y << 16, res[3] = r.y & 0xFFFF0000u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m + 32 * i < q.M) res[i] = (uint32_t)src[32 * i] << 16;
       }
     }
-    const long long row = j0 + j;
+    float4 f[kMaxSplit];
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s) {                   // all in flight together
+      if (s >= parts) continue;
+      const uint32_t peer = S > 1 ? mapa_shared(at, (uint32_t)s) : at;
+      if (vec) {
+        f[s] = ld_cluster_f4(peer);
+      } else {
+        f[s] = make_float4(ld_cluster_f1(peer), ld_cluster_f1(peer + 128), ld_cluster_f1(peer + 256), ld_cluster_f1(peer + 384));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s)
+      if (s < parts) v[0] += f[s].x, v[1] += f[s].y, v[2] += f[s].z, v[3] += f[s].w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += bias[i];
-    if (whole) {
-      if (p.ep.z)
-        *reinterpret_cast<uint2*>(p.ep.z + row * p.ep.ldz + m) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    float y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = act_of<ACT>(v[i]);
-      if (p.ep.residual) {
-        const uint2 r = *reinterpret_cast<const uint2*>(p.ep.residual + row * p.ep.ldr + m);
-        const float2 a = bf16x2_to_f32x2(r.x), b = bf16x2_to_f32x2(r.y);
-        v[0] += a.x, v[1] += a.y, v[2] += b.x, v[3] += b.y;
-      }
-      *reinterpret_cast<uint2*>(p.ep.out + row * p.ep.ldo + m) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    for (int i = 0; i < 4; ++i) y[i] = act_of<ACT>(v[i]);
+    if (ep.residual)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] += __uint_as_float(res[i]);
+    if (vec) {
+      if (ep.z) *reinterpret_cast<uint2*>(ep.z + row * ep.ldz + m) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(ep.out + row * ep.ldo + m) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (m + i >= p.M) break;
-        if (p.ep.z) p.ep.z[row * p.ep.ldz + m + i] = f32_to_bf16_bits(v[i]);
-        float y = act_of<ACT>(v[i]);
-        if (p.ep.residual) y += bf16_bits_to_f32(p.ep.residual[row * p.ep.ldr + m + i]);
-        p.ep.out[row * p.ep.ldo + m + i] = f32_to_bf16_bits(y);
+        const int c = m + 32 * i;
+        if (c >= q.M) break;
+        if (ep.z) ep.z[row * ep.ldz + c] = f32_to_bf16_bits(v[i]);
+        ep.out[row * ep.ldo + c] = f32_to_bf16_bits(y[i]);
       }
     }
   }
@@ -340,7 +375,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 }
 
 // ---------------------------------------------------------------- pair kernel
-// Many rows: 256 x bn tiles (bn up to 256) on CTA pairs, out[m, n] with the
+// Many rows: 256 x bn tiles (bn = 256 or 128) on CTA pairs, out[m, n] with the
 // token (or dW's row) on the accumulator's lanes. One persistent pair per two
 // SMs walks the tiles; the even CTA issues M = 256 MMAs (cta_group::2) on
 // operands both CTAs load, so each CTA brings its 128 rows of A and half of B.
@@ -351,8 +386,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // tiles in one list leave one ragged last round instead of two.
 // Warps: 0 and 3 = TMA producers of A and of B, 1 = MMA issuer (even CTA), 2 =
 // TMEM allocator, then db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
-// 64 columns at a time go through a swizzled 32-row box in shared memory, so
-// that global loads and stores are whole 128-byte lines whatever the pitch.
+// 64 columns at a time go through a swizzled 32-row box in shared memory, from
+// which one tensor store writes them (2-byte stores where the pitch is no
+// multiple of 16 bytes).
 // Every wait is bounded. No TMA load uses cluster multicast.
 
 constexpr int kPairM = 256;
@@ -369,6 +405,7 @@ static_assert(kPairSmem <= kMaxDynamicSmem, "shared memory");
 
 struct PairProblem {
   CUtensorMap tma_a, tma_b;
+  CUtensorMap tma_out, tma_z;  // of the output and z where their rows allow it (ep.vec): box 64 x 32 rows
   Epilogue ep;
   int M, N;
   int ksteps;
@@ -429,29 +466,30 @@ RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
   return reinterpret_cast<uint16_t*>(box_at(box, row, col >> 3)) + (col & 7);
 }
 
-// rows x cols of the box to global memory (whole warp). vec: 16-byte rows.
-RNX_DEVICE void box_store(uint8_t* box, uint16_t* dst, long long ld, int rows, int cols, int vec, int lane) {
-  __syncwarp();
+// The box to global memory at column col0, row row0 (whole warp): one tensor
+// store, which ends at the tensor's edges by itself, or rows x cols elements
+// where the pitch rules a tensor map out. Before the box is written again:
+// box_free().
+RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, long long ld, int row0, int col0, int rows,
+                          int cols, int vec, int lane) {
   if (vec) {
-    const int c = lane & 7, left = cols - 8 * c;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r < rows && left > 0) {
-        uint16_t* p = dst + r * ld + 8 * c;
-        if (left >= 8)
-          *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(box_at(box, r, c));
-        else
-          for (int e = 0; e < left; ++e) p[e] = *box_elem(box, r, 8 * c + e);
-      }
+    fence_proxy_async_smem();                 // the lanes' writes, visible to the tensor store
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, col0, row0, box);
+      bulk_commit_group();
     }
   } else {
+    __syncwarp();
     for (int r = 0; r < rows; ++r) {
-      uint16_t* p = dst + r * ld;
+      uint16_t* p = out + (row0 + r) * ld + col0;
       if (lane < cols) p[lane] = *box_elem(box, r, lane);
       if (lane + 32 < cols) p[lane + 32] = *box_elem(box, r, lane + 32);
     }
   }
+}
+RNX_DEVICE void box_free(int lane) {
+  if (lane == 0) bulk_wait_read_all();
   __syncwarp();
 }
 
@@ -546,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int first = is_a ? mt * kPairM + 128 * (int)rank : nt * p.bn + half * (int)rank;   // row of the operand
       const int ksteps = q.ksteps;
       const bool mn = is_a ? q.a_mn : q.b_mn;
-      const bool two = is_a || half > 64;          // MN-major blocks are 64 wide (then half is 64 or 128)
+      const bool two = is_a || half > 64;          // MN-major blocks are 64 wide
       const bool expects = is_a && rank == 0;
       for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
         if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
@@ -619,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int qd = warp & 3, ch = (warp - kFirstEpiWarp) >> 2;
     const uint32_t acc_empty_even[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
     uint8_t* box = smem + (size_t)kPairStages * kPairStageBytes + (size_t)(warp - kFirstEpiWarp) * kEpiBox;
-    const int chunks = (half + 63) / 64;           // 64-column chunks of this warp, the last may be narrower
+    const int chunks = half / 64;                  // 64-column chunks of this warp
     int tc = 0;
     PairTile t;
     for (int i = 0; pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
@@ -632,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int rows = min(32, q.M - row0);        // <= 0: none of this warp's rows exist
       bool gone = false;
       for (int c = 0; c < chunks; ++c) {
-        const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(min(64, half - 64 * c), q.N - col0);
+        const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(64, q.N - col0);
         BoxLoad res;
         const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
         if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);
@@ -674,6 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
         }
+        box_free(lane);                            // the previous chunk's store has read the box
         if (ep.z) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -682,7 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                            pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
                            pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
                            pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
-          box_store(box, ep.z + row0 * ep.ldz + col0, ep.ldz, rows, cols, ep.vec, lane);
+          box_store(box, &q.tma_z, ep.z, ep.ldz, row0, col0, rows, cols, ep.vec, lane);
+          box_free(lane);
         }
         if (res_src) {
           if (ep.vec) box_land(res, box, lane);
@@ -706,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           *at = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                            pack_bf16x2(y[6], y[7]));
         }
-        box_store(box, ep.out + row0 * ep.ldo + col0, ep.ldo, rows, cols, ep.vec, lane);
+        box_store(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
       }
       if (gone) {
         if (lane == 0) {
@@ -716,6 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         break;
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   // no CTA leaves (or frees TMEM) while the pair's MMAs or copies may still
@@ -873,13 +914,21 @@ bool operand_map(CUtensorMap* m, const Operand& o, int red, int box_rows) {
                             CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)o.ld);
 }
 
+// One product out[m, n] = epilogue(sum_r A[m, r] B[n, r]), row m of the output
+// contiguous along n.
+struct Product {
+  Operand a, b;
+  int red;
+  Epilogue ep;
+};
+
 template <int ACT>
-cudaError_t launch_split_act(const SplitParams& p, int S, int smem, cudaStream_t st) {
+cudaError_t launch_split_act(const SplitParams& p, int smem, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(linear_split_kernel<ACT>, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S, (p.M + kTileM - 1) / kTileM, (p.J + p.bn - 1) / p.bn);
+  cfg.gridDim = dim3((unsigned)(p.S * p.tiles));
   cfg.blockDim = dim3(kSplitThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -889,7 +938,7 @@ cudaError_t launch_split_act(const SplitParams& p, int S, int smem, cudaStream_t
   attr[1].id = cudaLaunchAttributePriority;
   attr[1].val.priority = launch_priority_high();
   attr[2].id = cudaLaunchAttributeClusterDimension;
-  attr[2].val.clusterDim.x = S;
+  attr[2].val.clusterDim.x = p.S;
   attr[2].val.clusterDim.y = 1;
   attr[2].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -897,55 +946,66 @@ cudaError_t launch_split_act(const SplitParams& p, int S, int smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, linear_split_kernel<ACT>, p);
 }
 
-// out[j, m] = epilogue(sum_r A[m, r] B[j, r])
-cudaError_t launch_split(int act, const Operand& a, const Operand& b, int red, const Epilogue& ep, const DbJoin& db,
-                         uint32_t* status, bool clear, cudaStream_t st) {
+// The products' columns are the split kernel's m side, their rows its j side.
+cudaError_t launch_split(int act, const Product* prod, int n, const DbJoin& db, uint32_t* status, bool clear,
+                         cudaStream_t st) {
   SplitParams p;
   memset(&p, 0, sizeof p);
-  const int J = b.rows, unit = b.mn ? 64 : 16;            // MN-major blocks are 64 wide
-  const int jt = (J + 255) / 256;
-  p.bn = ((J + jt - 1) / jt + unit - 1) / unit * unit;
-  p.M = a.rows;
-  p.J = J;
-  p.ksteps = (red + kStepK - 1) / kStepK;
-  const int mt = (p.M + kTileM - 1) / kTileM, tiles = mt * ((J + p.bn - 1) / p.bn);
-  const int stage = kABytes + p.bn * 128;
+  long long tiles = 0;
+  int stage[2] = {0, 0}, most_steps = 1, widest = 0;
+  for (int i = 0; i < n; ++i) {
+    SplitProblem& q = p.prob[i];
+    const Operand &a = prod[i].b, &b = prod[i].a;
+    const int J = b.rows, unit = b.mn ? 64 : 16;            // MN-major blocks are 64 wide
+    const int jt = (J + 255) / 256;
+    q.bn = ((J + jt - 1) / jt + unit - 1) / unit * unit;
+    q.M = a.rows;
+    q.J = J;
+    q.ksteps = (prod[i].red + kStepK - 1) / kStepK;
+    q.mt = (q.M + kTileM - 1) / kTileM;
+    const long long t = (long long)q.mt * ((J + q.bn - 1) / q.bn);
+    tiles += t;
+    if (tiles > 1 << 27) return cudaErrorInvalidValue;
+    q.tiles = (int)t;
+    q.a_mn = a.mn;
+    q.b_mn = b.mn;
+    q.ep = prod[i].ep;
+    stage[i] = kABytes + q.bn * 128;
+    most_steps = std::max(most_steps, q.ksteps);
+    widest = std::max(widest, q.bn);
+    if (!operand_map(&q.tma_a, a, prod[i].red, kTileM) || !operand_map(&q.tma_b, b, prod[i].red, q.bn))
+      return cudaErrorInvalidValue;
+  }
   // narrow tiles keep two CTAs per SM (one's epilogue beside the other's
   // stream), wide ones need the shared memory for their stages
-  const bool two = p.bn <= 64;
+  const bool two = widest <= 64;
   const int budget = two ? 100 * 1024 : 200 * 1024;
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= (two ? 2 : 1) * kNumSMs && S * 2 <= p.ksteps) S *= 2;
-  const int steps = (p.ksteps + S - 1) / S;
-  const int hold = (p.bn * kTileM * 4 + stage - 1) / stage;          // stages that the fp32 tile takes
-  p.stages = std::max(hold, std::min({budget / stage, steps, kSplitMaxStages}));
+  while (S < kMaxSplit && tiles * S * 2 <= (two ? 2 : 1) * kNumSMs && S * 2 <= most_steps) S *= 2;
+  int smem = 0;
+  for (int i = 0; i < n; ++i) {
+    SplitProblem& q = p.prob[i];
+    const int steps = (q.ksteps + S - 1) / S;
+    const int hold = (q.bn * kTileM * 4 + stage[i] - 1) / stage[i];          // stages that the fp32 tile takes
+    q.stages = std::max(hold, std::min({budget / stage[i], steps, kSplitMaxStages}));
+    smem = std::max(smem, q.stages * stage[i] + 1024);
+  }
   p.tmem_cols = 32;
-  while (p.tmem_cols < p.bn) p.tmem_cols *= 2;
-  p.a_mn = a.mn;
-  p.b_mn = b.mn;
-  p.ep = ep;
+  while (p.tmem_cols < widest) p.tmem_cols *= 2;
+  p.S = S;
+  p.tiles = (int)tiles;
   p.db = db;
   p.status = status;
   p.clear = clear;
-  if (mt > 65535 || (J + p.bn - 1) / p.bn > 65535) return cudaErrorInvalidValue;
-  if (!operand_map(&p.tma_a, a, red, kTileM) || !operand_map(&p.tma_b, b, red, p.bn)) return cudaErrorInvalidValue;
-  const int smem = p.stages * stage + 1024;
   switch (act) {
-    case MOE_ACT_NONE: return launch_split_act<MOE_ACT_NONE>(p, S, smem, st);
-    case MOE_ACT_RELU: return launch_split_act<MOE_ACT_RELU>(p, S, smem, st);
-    case MOE_ACT_GELU: return launch_split_act<MOE_ACT_GELU>(p, S, smem, st);
-    case MOE_ACT_GELU_TANH: return launch_split_act<MOE_ACT_GELU_TANH>(p, S, smem, st);
-    case MOE_ACT_SILU: return launch_split_act<MOE_ACT_SILU>(p, S, smem, st);
+    case MOE_ACT_NONE: return launch_split_act<MOE_ACT_NONE>(p, smem, st);
+    case MOE_ACT_RELU: return launch_split_act<MOE_ACT_RELU>(p, smem, st);
+    case MOE_ACT_GELU: return launch_split_act<MOE_ACT_GELU>(p, smem, st);
+    case MOE_ACT_GELU_TANH: return launch_split_act<MOE_ACT_GELU_TANH>(p, smem, st);
+    case MOE_ACT_SILU: return launch_split_act<MOE_ACT_SILU>(p, smem, st);
   }
   return cudaErrorInvalidValue;
 }
-
-// One product out[m, n] = epilogue(sum_r A[m, r] B[n, r]) of a pair launch.
-struct Product {
-  Operand a, b;
-  int red;
-  Epilogue ep;
-};
 
 template <int ACT>
 cudaError_t launch_pair_act(const PairParams& p, int pairs, cudaStream_t st) {
@@ -974,6 +1034,12 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
     tiles[i] = (long long)q.mt * q.nt;
     if (tiles[i] > 1 << 30) return cudaErrorInvalidValue;
     if (!operand_map(&q.tma_a, prod[i].a, prod[i].red, kTileM) || !operand_map(&q.tma_b, prod[i].b, prod[i].red, bn / 2))
+      return cudaErrorInvalidValue;
+    auto out_map = [&](CUtensorMap* m, const uint16_t* out, long long ld) {
+      return make_tensor_map_2d(m, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)q.N, (uint64_t)q.M, 64, 32,
+                                CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)ld);
+    };
+    if (q.ep.vec && (!out_map(&q.tma_out, q.ep.out, q.ep.ldo) || (q.ep.z && !out_map(&q.tma_z, q.ep.z, q.ep.ldz))))
       return cudaErrorInvalidValue;
   }
   p.tiles0 = (int)tiles[0];
@@ -1090,11 +1156,10 @@ cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t s
   if (e != cudaSuccess) return e;
   Epilogue ep{a.bias, a.residual, a.z, a.y, a.ldr, a.ldz, a.ldy, 0};
   ep.vec = vec_ok(ep);
-  if (const int bn = pair_width(a.T, a.N)) {
-    const Product prod{x, w, a.K, ep};
-    return launch_pair(act, &prod, 1, bn, DbJoin{}, reinterpret_cast<uint32_t*>(base), pk.n == 0, st);
-  }
-  return launch_split(act, w, x, a.K, ep, DbJoin{}, reinterpret_cast<uint32_t*>(base), pk.n == 0, st);
+  const Product prod{x, w, a.K, ep};
+  uint32_t* status = reinterpret_cast<uint32_t*>(base);
+  if (const int bn = pair_width(a.T, a.N)) return launch_pair(act, &prod, 1, bn, DbJoin{}, status, pk.n == 0, st);
+  return launch_split(act, &prod, 1, DbJoin{}, status, pk.n == 0, st);
 }
 
 cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* ws, cudaStream_t st) {
@@ -1149,32 +1214,32 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (a.db) db = DbJoin{part, a.db, chunks, a.N};
   }
-  Product pair[2];
-  int pairs = 0, width = 0;
-  auto product = [&](bool is_dx) {
-    Epilogue ep{nullptr, nullptr, nullptr, is_dx ? a.dx : a.dw, 0, 0, is_dx ? a.lddx : a.lddw, 0};
+  // one launch for the products of either kernel
+  Product wide[2], few[2];
+  int n_wide = 0, n_few = 0, width = 0;
+  auto take = [&](uint16_t* out, long long ldo, const Operand& rows, const Operand& cols, int red) {
+    Epilogue ep{nullptr, nullptr, nullptr, out, 0, 0, ldo, 0};
     ep.vec = vec_ok(ep);
-    // out[t, k] = sum_n dz[t, n] w[n, k];  out[n, k] = sum_t dz[t, n] x[t, k]
-    return is_dx ? Product{Operand{dz, lddz, a.T, false}, Operand{w, ldw, a.K, true}, a.N, ep}
-                 : Product{Operand{dz, lddz, a.N, true}, Operand{x, ldx, a.K, true}, a.T, ep};
-  };
-  for (int i = 0; i < 2; ++i) {
-    if (!(i == 0 ? a.dx : a.dw)) continue;
-    const Product q = product(i == 0);
-    if (const int bn = pair_width(q.a.rows, q.b.rows)) {
-      pair[pairs++] = q;
+    if (const int bn = pair_width(rows.rows, cols.rows)) {
+      wide[n_wide++] = Product{rows, cols, red, ep};
       width = bn;
-      continue;
+    } else {
+      few[n_few++] = Product{rows, cols, red, ep};
     }
-    // the split kernel's tiles have the product's rows on its j side
-    e = launch_split(MOE_ACT_NONE, q.b, q.a, q.red, q.ep, db, status, clear, st);
-    if (e != cudaSuccess) return e;
+  };
+  // dx[t, k] = sum_n dz[t, n] w[n, k];  dw[n, k] = sum_t dz[t, n] x[t, k]
+  if (a.dx) take(a.dx, a.lddx, Operand{dz, lddz, a.T, false}, Operand{w, ldw, a.K, true}, a.N);
+  if (a.dw) take(a.dw, a.lddw, Operand{dz, lddz, a.N, true}, Operand{x, ldx, a.K, true}, a.T);
+  // the products with the longer tiles first
+  if (n_wide == 2 && wide[0].red < wide[1].red) std::swap(wide[0], wide[1]);
+  if (n_few == 2 && few[0].red < few[1].red) std::swap(few[0], few[1]);
+  if (n_wide) {
+    if ((e = launch_pair(MOE_ACT_NONE, wide, n_wide, width, db, status, clear, st)) != cudaSuccess) return e;
     db = DbJoin{};
     clear = false;
   }
-  if (pairs == 2 && pair[0].red < pair[1].red) std::swap(pair[0], pair[1]);   // the longer tiles first
-  if (pairs) {
-    if ((e = launch_pair(MOE_ACT_NONE, pair, pairs, width, db, status, clear, st)) != cudaSuccess) return e;
+  if (n_few) {
+    if ((e = launch_split(MOE_ACT_NONE, few, n_few, db, status, clear, st)) != cudaSuccess) return e;
     db = DbJoin{};
   }
   if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);

@@ -196,6 +196,12 @@ RNX_DEVICE float4 ld_cluster_f4(uint32_t cluster_addr) {
   return v;
 }
 
+RNX_DEVICE float ld_cluster_f1(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 RNX_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
