@@ -54,19 +54,30 @@ RNX_DEVICE float act_of(float z) {
   return z;
 }
 
-// The slope, for the HBM-bound dz pass.
+// The slope from the same forms (normcdff, tanhf and full divisions took the
+// dz pass to 3.3 times its HBM time). With E = exp(-v) and s = 1 / (1 + E),
+// 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0.
 template <int ACT>
 RNX_DEVICE float act_grad(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-  if (ACT == MOE_ACT_GELU) return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), normcdff(z));
+  if (ACT == MOE_ACT_GELU) {                               // Phi(z) + z phi(z)
+    const float x = fabsf(z) * 0.7071067811865476f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                0.254829592f);
+    const float g = __expf(-x * x);
+    const float tail = 0.5f * poly * g;
+    return fmaf(z * 0.3989422804014327f, g, z > 0.f ? 1.f - tail : tail);
+  }
   if (ACT == MOE_ACT_GELU_TANH) {
     const float z2 = z * z;
-    const float t = tanhf(0.7978845608028654f * fmaf(0.044715f * z2, z, z));
-    return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.7978845608028654f * fmaf(3.f * 0.044715f, z2, 1.f);
+    const float E = __expf(-1.5957691216057308f * fmaf(0.044715f * z2, z, z));
+    const float s = __fdividef(1.f, 1.f + E);
+    return fmaf(z * s * fminf(E * s, 1.f), 1.5957691216057308f * fmaf(3.f * 0.044715f, z2, 1.f), s);
   }
   if (ACT == MOE_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-z));
-    return s * fmaf(z, 1.f - s, 1.f);
+    const float E = __expf(-z), s = __fdividef(1.f, 1.f + E);
+    return fmaf(z * s, fminf(E * s, 1.f), s);
   }
   return 1.f;
 }
@@ -773,8 +784,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------- dz and db
 // dz = dy act'(z) in bf16 and the column sums of each chunk of rows in fp32
 // (rows of a warp in order, then the warps). A CTA owns 256 columns of one
-// chunk. VEC: 16-byte loads, eight consecutive columns per lane; otherwise
-// columns lane + 32 i. HBM-bound: 6 T N bytes (dy, z, dz).
+// chunk; a warp has four rows' loads in flight together. VEC: 16-byte loads,
+// eight consecutive columns per lane; otherwise columns lane + 32 i. HBM-bound:
+// 6 T N bytes (dy, z, dz).
+constexpr int kDzRows = 4;
+
+RNX_DEVICE void unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = bf16x2_to_f32x2(w[i]);
+    f[2 * i] = v.x, f[2 * i + 1] = v.y;
+  }
+}
+
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long long lddy, const uint16_t* z,
                                                         long long ldz, int T, int N, int rows_per_cta, uint16_t* dz,
@@ -789,42 +812,43 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long
   pdl_wait();
   pdl_trigger();
   if (clear && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) *clear = 0u;
-#pragma unroll 2
-  for (int r = r0 + warp; r < r1; r += 8) {
-    float g[8], a[8];
-    const uint16_t* py = dy + r * lddy;
-    const uint16_t* pz = z + r * ldz;
-    if (whole) {
-      const uint4 u = *reinterpret_cast<const uint4*>(py + c0);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int base = r0 + warp; base < r1; base += 8 * kDzRows) {
+    uint4 u[kDzRows], uz[kDzRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = bf16x2_to_f32x2(w[i]);
-        g[2 * i] = f.x, g[2 * i + 1] = f.y;
-      }
-      if (ACT != MOE_ACT_NONE) {
-        const uint4 uz = *reinterpret_cast<const uint4*>(pz + c0);
-        const uint32_t wz[4] = {uz.x, uz.y, uz.z, uz.w};
+    for (int k = 0; k < kDzRows; ++k) {
+      const int r = base + 8 * k;
+      u[k] = uz[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= r1) continue;
+      const uint16_t* py = dy + r * lddy;
+      const uint16_t* pz = z + r * ldz;
+      if (whole) {
+        u[k] = *reinterpret_cast<const uint4*>(py + c0);
+        if (ACT != MOE_ACT_NONE) uz[k] = *reinterpret_cast<const uint4*>(pz + c0);
+      } else {
+        uint32_t a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = bf16x2_to_f32x2(wz[i]);
-          a[2 * i] = f.x, a[2 * i + 1] = f.y;
+        for (int i = 0; i < 8; ++i) {
+          const int c = c0 + kStep * i;
+          a[i] = c < N ? py[c] : 0u;
+          b[i] = ACT != MOE_ACT_NONE && c < N ? pz[c] : 0u;
         }
+        u[k] = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
+        uz[k] = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
       }
-    } else {
+    }
+#pragma unroll
+    for (int k = 0; k < kDzRows; ++k) {
+      const int r = base + 8 * k;
+      if (r >= r1) break;
+      float g[8], a[8];
+      unpack8(u[k], g);
+      if (ACT != MOE_ACT_NONE) unpack8(uz[k], a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = c0 + kStep * i;
-        g[i] = c < N ? bf16_bits_to_f32(py[c]) : 0.f;
-        a[i] = ACT != MOE_ACT_NONE && c < N ? bf16_bits_to_f32(pz[c]) : 0.f;
+        if (ACT != MOE_ACT_NONE) g[i] *= act_grad<ACT>(a[i]);
+        acc[i] += g[i];
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (ACT != MOE_ACT_NONE) g[i] *= act_grad<ACT>(a[i]);
-      acc[i] += g[i];
-    }
-    if (dz) {
+      if (!dz) continue;
       uint16_t* pd = dz + r * lddz;
       if (whole) {
         *reinterpret_cast<uint4*>(pd + c0) = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
@@ -957,12 +981,15 @@ cudaError_t launch_split(int act, const Product* prod, int n, const DbJoin& db, 
     SplitProblem& q = p.prob[i];
     const Operand &a = prod[i].b, &b = prod[i].a;
     const int J = b.rows, unit = b.mn ? 64 : 16;            // MN-major blocks are 64 wide
-    const int jt = (J + 255) / 256;
-    q.bn = ((J + jt - 1) / jt + unit - 1) / unit * unit;
     q.M = a.rows;
     q.J = J;
     q.ksteps = (prod[i].red + kStepK - 1) / kStepK;
     q.mt = (q.M + kTileM - 1) / kTileM;
+    // the widest tiles (up to 256), narrower ones down to 64 while the tiles
+    // and the splits they allow leave SMs idle
+    int jt = (J + 255) / 256;
+    while ((long long)q.mt * jt * std::min(kMaxSplit, q.ksteps) < kNumSMs && (J + jt - 1) / jt > 64) ++jt;
+    q.bn = ((J + jt - 1) / jt + unit - 1) / unit * unit;
     const long long t = (long long)q.mt * ((J + q.bn - 1) / q.bn);
     tiles += t;
     if (tiles > 1 << 27) return cudaErrorInvalidValue;
@@ -1105,11 +1132,12 @@ cudaError_t launch_dz(bool vec, dim3 grid, cudaStream_t st, const uint16_t* dy, 
                     clear);
 }
 
-// Row chunks of the dz pass: enough CTAs to fill the GPU a few times over.
+// Rows per CTA of the dz pass: one round of loads, more where that gives over
+// eight CTAs per SM.
 int dz_rows(int T, int N) {
-  const long long strips = (N + 255) / 256;
-  const long long chunks = std::max<long long>(1, std::min<long long>((T + 31) / 32, (8 * kNumSMs + strips - 1) / strips));
-  return (int)((T + chunks - 1) / chunks);
+  const long long round = 8 * kDzRows, strips = (N + 255) / 256;
+  const long long rounds = ((T + round - 1) / round * strips + 8 * kNumSMs - 1) / (8 * kNumSMs);
+  return (int)(round * rounds);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
