@@ -970,55 +970,130 @@ cudaError_t launch_split_act(const SplitParams& p, int smem, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, linear_split_kernel<ACT>, p);
 }
 
+// ---------------------------------------------------------------- choice of kernel and tiles
+// Estimated times in microseconds at 1.9 GHz, fitted to 90 measured
+// combinations of shape (1 to 5000 tokens, 256 to 12288 features), tile width
+// and split; the choices by them took 0.6% longer on average than the best
+// measured ones. What they weigh: narrow tiles and deep splits use more SMs
+// but stream A more often and fill more than one wave; the pair kernel reads
+// least and overlaps its epilogue but needs many tiles.
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+struct SplitPlan {
+  double us;
+  int S;
+  int bn[2];
+};
+
+// CTAs of clusters of S that are resident together, for tiles of up to 64
+// columns (two CTAs per SM) or wider.
+int split_capacity(bool two, int S) {
+  return two ? (S <= 2 ? 296 : S == 4 ? 264 : 256) : (S <= 2 ? 148 : S == 4 ? 136 : 112);
+}
+
+int tile_width(const Product& q, int most) {
+  const int J = q.a.rows, unit = q.a.mn ? 64 : 16;           // MN-major blocks are 64 wide
+  const long long jt = ceil_div(J, most);
+  return (int)(ceil_div(ceil_div(J, jt), unit) * unit);
+}
+
+SplitPlan plan_split(const Product* prod, int n) {
+  SplitPlan best{};
+  best.us = -1;
+  for (int most = 256; most >= 16; most /= 2) {
+    if (most < 64 && (prod[0].a.mn || (n > 1 && prod[1].a.mn))) break;
+    if (most < 32 && prod[0].a.rows > 16) break;
+    int bn[2] = {0, 0}, widest = 0;
+    long long tiles = 0;
+    for (int i = 0; i < n; ++i) {
+      bn[i] = tile_width(prod[i], most);
+      widest = std::max(widest, bn[i]);
+      tiles += ceil_div(prod[i].b.rows, kTileM) * ceil_div(prod[i].a.rows, bn[i]);
+    }
+    const bool two = widest <= 64;
+    for (int S = 1; S <= kMaxSplit; S *= 2) {
+      const int cap = split_capacity(two, S);
+      const bool shared = two && tiles * S > kNumSMs;        // two CTAs share an SM's bandwidth
+      double longest = 0, sum = 0;
+      for (int i = 0; i < n; ++i) {
+        const long long t = ceil_div(prod[i].b.rows, kTileM) * ceil_div(prod[i].a.rows, bn[i]);
+        const double kb = 16 + bn[i] / 8.0, steps = (double)ceil_div(ceil_div(prod[i].red, kStepK), S);
+        const double us = steps * kb * (two ? (shared ? 0.0174 : 0.0126) : 0.0091) + 0.0196 * bn[i] + 0.0197 * bn[i] / S + 2.85;
+        longest = std::max(longest, us);
+        sum += us * t / tiles;
+      }
+      const long long waves = ceil_div(tiles * S, cap);
+      const double us = 0.9 + (waves == 1 ? longest : waves * sum);
+      if (best.us < 0 || us < best.us) best = SplitPlan{us, S, {bn[0], bn[1]}};
+    }
+  }
+  return best;
+}
+
+// A round of the pair kernel takes the longer of its products and its epilogue.
+double pair_us(const Product* prod, int n, int bn) {
+  long long tiles = 0;
+  double sum = 0;
+  for (int i = 0; i < n; ++i) {
+    const long long t = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
+    const double steps = (double)ceil_div(prod[i].red, kStepK);
+    sum += t * std::max(steps * (bn == 256 ? 0.28 : 0.195), bn == 256 ? 2.4 : 1.4);
+    tiles += t;
+  }
+  const long long rounds = ceil_div(tiles, kNumSMs / 2);
+  return (bn == 256 ? 8.1 : 6.5) + rounds * (sum / tiles) + 0.5 * (rounds - 1);
+}
+
+struct Choice {
+  double us;
+  int width;           // of the pair kernel's tiles, 0 for the split kernel
+  SplitPlan split;
+};
+Choice choose(const Product* prod, int n) {
+  Choice c{0, 0, plan_split(prod, n)};
+  c.us = c.split.us;
+  for (int bn = 128; bn <= 256; bn *= 2) {
+    const double us = pair_us(prod, n, bn);
+    if (us < c.us) c.us = us, c.width = bn;
+  }
+  return c;
+}
+
 // The products' columns are the split kernel's m side, their rows its j side.
-cudaError_t launch_split(int act, const Product* prod, int n, const DbJoin& db, uint32_t* status, bool clear,
-                         cudaStream_t st) {
+cudaError_t launch_split(int act, const Product* prod, int n, const SplitPlan& plan, const DbJoin& db,
+                         uint32_t* status, bool clear, cudaStream_t st) {
   SplitParams p;
   memset(&p, 0, sizeof p);
+  const int S = plan.S;
+  const bool two = std::max(plan.bn[0], plan.bn[1]) <= 64;
+  const int budget = two ? 100 * 1024 : 200 * 1024;
   long long tiles = 0;
-  int stage[2] = {0, 0}, most_steps = 1, widest = 0;
+  int smem = 0;
+  p.tmem_cols = 32;
   for (int i = 0; i < n; ++i) {
     SplitProblem& q = p.prob[i];
     const Operand &a = prod[i].b, &b = prod[i].a;
-    const int J = b.rows, unit = b.mn ? 64 : 16;            // MN-major blocks are 64 wide
     q.M = a.rows;
-    q.J = J;
+    q.J = b.rows;
+    q.bn = plan.bn[i];
     q.ksteps = (prod[i].red + kStepK - 1) / kStepK;
     q.mt = (q.M + kTileM - 1) / kTileM;
-    // the widest tiles (up to 256), narrower ones down to 64 while the tiles
-    // and the splits they allow leave SMs idle
-    int jt = (J + 255) / 256;
-    while ((long long)q.mt * jt * std::min(kMaxSplit, q.ksteps) < kNumSMs && (J + jt - 1) / jt > 64) ++jt;
-    q.bn = ((J + jt - 1) / jt + unit - 1) / unit * unit;
-    const long long t = (long long)q.mt * ((J + q.bn - 1) / q.bn);
+    const long long t = (long long)q.mt * ((q.J + q.bn - 1) / q.bn);
     tiles += t;
     if (tiles > 1 << 27) return cudaErrorInvalidValue;
     q.tiles = (int)t;
     q.a_mn = a.mn;
     q.b_mn = b.mn;
     q.ep = prod[i].ep;
-    stage[i] = kABytes + q.bn * 128;
-    most_steps = std::max(most_steps, q.ksteps);
-    widest = std::max(widest, q.bn);
+    const int stage = kABytes + q.bn * 128, steps = (q.ksteps + S - 1) / S;
+    const int hold = (q.bn * kTileM * 4 + stage - 1) / stage;          // stages that the fp32 tile takes
+    q.stages = std::max(hold, std::min({budget / stage, steps, kSplitMaxStages}));
+    smem = std::max(smem, q.stages * stage + 1024);
+    while (p.tmem_cols < q.bn) p.tmem_cols *= 2;
     if (!operand_map(&q.tma_a, a, prod[i].red, kTileM) || !operand_map(&q.tma_b, b, prod[i].red, q.bn))
       return cudaErrorInvalidValue;
   }
-  // narrow tiles keep two CTAs per SM (one's epilogue beside the other's
-  // stream), wide ones need the shared memory for their stages
-  const bool two = widest <= 64;
-  const int budget = two ? 100 * 1024 : 200 * 1024;
-  int S = 1;
-  while (S < kMaxSplit && tiles * S * 2 <= (two ? 2 : 1) * kNumSMs && S * 2 <= most_steps) S *= 2;
-  int smem = 0;
-  for (int i = 0; i < n; ++i) {
-    SplitProblem& q = p.prob[i];
-    const int steps = (q.ksteps + S - 1) / S;
-    const int hold = (q.bn * kTileM * 4 + stage[i] - 1) / stage[i];          // stages that the fp32 tile takes
-    q.stages = std::max(hold, std::min({budget / stage[i], steps, kSplitMaxStages}));
-    smem = std::max(smem, q.stages * stage[i] + 1024);
-  }
-  p.tmem_cols = 32;
-  while (p.tmem_cols < widest) p.tmem_cols *= 2;
   p.S = S;
   p.tiles = (int)tiles;
   p.db = db;
@@ -1098,11 +1173,6 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
     case MOE_ACT_SILU: return launch_pair_act<MOE_ACT_SILU>(p, pairs, st);
   }
   return cudaErrorInvalidValue;
-}
-
-// The width of the pair kernel's tiles for m x n outputs, 0 for the split kernel.
-int pair_width(int m, int n) {
-  return m > 512 && n > 512 ? 256 : 0;
 }
 
 bool vec_ok(const Epilogue& e) {
@@ -1186,8 +1256,9 @@ cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t s
   ep.vec = vec_ok(ep);
   const Product prod{x, w, a.K, ep};
   uint32_t* status = reinterpret_cast<uint32_t*>(base);
-  if (const int bn = pair_width(a.T, a.N)) return launch_pair(act, &prod, 1, bn, DbJoin{}, status, pk.n == 0, st);
-  return launch_split(act, &prod, 1, DbJoin{}, status, pk.n == 0, st);
+  const Choice c = choose(&prod, 1);
+  if (c.width) return launch_pair(act, &prod, 1, c.width, DbJoin{}, status, pk.n == 0, st);
+  return launch_split(act, &prod, 1, c.split, DbJoin{}, status, pk.n == 0, st);
 }
 
 cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* ws, cudaStream_t st) {
@@ -1242,33 +1313,36 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (a.db) db = DbJoin{part, a.db, chunks, a.N};
   }
-  // one launch for the products of either kernel
-  Product wide[2], few[2];
-  int n_wide = 0, n_few = 0, width = 0;
+  Product prod[2];
+  int n = 0;
   auto take = [&](uint16_t* out, long long ldo, const Operand& rows, const Operand& cols, int red) {
     Epilogue ep{nullptr, nullptr, nullptr, out, 0, 0, ldo, 0};
     ep.vec = vec_ok(ep);
-    if (const int bn = pair_width(rows.rows, cols.rows)) {
-      wide[n_wide++] = Product{rows, cols, red, ep};
-      width = bn;
-    } else {
-      few[n_few++] = Product{rows, cols, red, ep};
-    }
+    prod[n++] = Product{rows, cols, red, ep};
   };
   // dx[t, k] = sum_n dz[t, n] w[n, k];  dw[n, k] = sum_t dz[t, n] x[t, k]
   if (a.dx) take(a.dx, a.lddx, Operand{dz, lddz, a.T, false}, Operand{w, ldw, a.K, true}, a.N);
   if (a.dw) take(a.dw, a.lddw, Operand{dz, lddz, a.N, true}, Operand{x, ldx, a.K, true}, a.T);
-  // the products with the longer tiles first
-  if (n_wide == 2 && wide[0].red < wide[1].red) std::swap(wide[0], wide[1]);
-  if (n_few == 2 && few[0].red < few[1].red) std::swap(few[0], few[1]);
-  if (n_wide) {
-    if ((e = launch_pair(MOE_ACT_NONE, wide, n_wide, width, db, status, clear, st)) != cudaSuccess) return e;
+  if (n == 2 && prod[0].red < prod[1].red) std::swap(prod[0], prod[1]);   // the longer tiles first
+  auto launch = [&](const Product* q, int count, const Choice& c) {
+    const cudaError_t err = c.width ? launch_pair(MOE_ACT_NONE, q, count, c.width, db, status, clear, st)
+                                    : launch_split(MOE_ACT_NONE, q, count, c.split, db, status, clear, st);
     db = DbJoin{};
     clear = false;
-  }
-  if (n_few) {
-    if ((e = launch_split(MOE_ACT_NONE, few, n_few, db, status, clear, st)) != cudaSuccess) return e;
-    db = DbJoin{};
+    return err;
+  };
+  if (n) {
+    // both in one launch, or one launch each where one wants the other kernel
+    const Choice both = choose(prod, n);
+    if (n == 2) {
+      const Choice first = choose(prod, 1), second = choose(prod + 1, 1);
+      if (!first.width != !second.width && first.us + second.us < both.us) {
+        if ((e = launch(prod, 1, first)) != cudaSuccess) return e;
+        if ((e = launch(prod + 1, 1, second)) != cudaSuccess) return e;
+        n = 0;
+      }
+    }
+    if (n && (e = launch(prod, n, both)) != cudaSuccess) return e;
   }
   if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);
   return cudaSuccess;
