@@ -328,11 +328,10 @@ cudaError_t launch_router_grad(const float* logits, const int32_t* ids, int T, i
 
 // ---------------------------------------------------------------- BF16 linear layer (linear.cu)
 
-// Workspace offsets: the status word, then what the call needs of the flags of
-// cut tiles, copies of x and w in 16-byte-aligned rows, dz, the partial
-// column sums of db and the partial sums of cut tiles.
+// Workspace offsets: the status word, then what the call needs of copies of x
+// and w in 16-byte-aligned rows, dz and the partial column sums of db.
 struct LinearLayout {
-  size_t flags, x, w, dz, db, parts, bytes;
+  size_t x, w, dz, part, bytes;
 };
 LinearLayout linear_layout(int T, int K, int N, long long ldx, long long ldw);
 LinearLayout linear_backward_layout(int T, int K, int N, long long ldx, long long ldw);

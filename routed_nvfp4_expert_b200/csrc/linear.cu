@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // Warps: 0 and 3 = TMA producers of A and of B, 1 = MMA issuer (even CTA), 2 =
 // TMEM allocator, then db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
 // 64 columns at a time go through a swizzled 32-row box in shared memory, from
-// which one tensor store writes them (2-byte stores where the pitch or N is no
-// multiple of 8 elements).
+// which one tensor store writes them (2-byte stores where the pitch is no
+// multiple of 16 bytes).
 // Every wait is bounded. No TMA load uses cluster multicast.
 
 constexpr int kPairM = 256;
@@ -416,83 +416,46 @@ static_assert(kPairSmem <= kMaxDynamicSmem, "shared memory");
 
 struct PairProblem {
   CUtensorMap tma_a, tma_b;
-  CUtensorMap tma_out, tma_z;  // of the output and z where rows and N allow it (ep.vec): box 64 x 32 rows
+  CUtensorMap tma_out, tma_z;  // of the output and z where their rows allow it (ep.vec): box 64 x 32 rows
   Epilogue ep;
   int M, N;
   int ksteps;
   int a_mn, b_mn;
   int mt, nt;                 // tiles
 };
-// How the tiles go to the pairs. Each pair takes a tile of every whole round.
-// What is left, fewer tiles than pairs, is one more round, in which a tile may
-// be cut along the reduction into up to kMaxCut equal pieces for as many
-// pairs: the others leave their fp32 partial sums in memory for the one with
-// the last steps, which adds them (nearest below first) and finishes the tile.
-// It waits for pairs of lower index alone, which were started before it and
-// wait for nobody. Equal pieces keep the pairs in step, so that they still
-// share the operands' slices in L2: one run of steps per pair, cut anywhere,
-// was slower than the ragged round that it saved (394 against 340 us at 4096 x
-// 12288 x 4096, whose rest of 34 tiles now takes half a round).
-constexpr int kMaxCut = 6;
-
 struct PairParams {
   PairProblem prob[2];
   DbJoin db;
   uint32_t* status;
-  float* parts;               // [pairs][2][8 warps][bn / 128][64 x 32] partial sums
-  uint32_t* flags;            // [pairs][2][8], zeroed before the launch
   int bn;
-  int tiles[2];
-  int rounds[2];              // whole rounds of either product
-  int cut[2];                 // pieces of each of its remaining tiles
+  int tiles0, tiles1;         // tiles of the two products (0: absent)
+  int rounds1;                // rounds of the second product in which every pair takes a tile; behind them
+                              // only pairs with fewer tiles of the first do (pairs >= first_light)
+  int first_light;
   int clear;
 };
 
-struct PairWork {
-  int which, index;           // product and tile
-  int k_lo, k_hi;             // its steps
-  int parts, stride;          // partial sums to add: of pair - stride, pair - 2 stride, ...
-  bool partial;               // leaves partial sums
+// The i-th tile of a pair: first the first product's, round robin, then the
+// second's. Returns false behind the last.
+struct PairTile {
+  int which, index;
 };
-// The i-th piece of work of a pair; false behind the last.
-RNX_DEVICE bool pair_work(const PairParams& p, int pair, int n_pairs, int i, PairWork& w) {
-  w.parts = 0;
-  w.stride = 1;
-  w.partial = false;
-  w.k_lo = 0;
-  for (int q = 0; q < 2; ++q) {
-    if (i < p.rounds[q]) {
-      w.which = q, w.index = i * n_pairs + pair, w.k_hi = p.prob[q].ksteps;
-      return true;
-    }
-    i -= p.rounds[q];
+RNX_DEVICE bool pair_tile(const PairParams& p, int pair, int n_pairs, int i, PairTile& t) {
+  const int n0 = pair < p.tiles0 ? (p.tiles0 - pair + n_pairs - 1) / n_pairs : 0;
+  if (i < n0) {
+    t.which = 0;
+    t.index = pair + i * n_pairs;
+    return true;
   }
-  int at = i * n_pairs + pair;
-  for (int q = 0; q < 2; ++q) {
-    const int rest = p.tiles[q] - p.rounds[q] * n_pairs, cut = p.cut[q], ks = p.prob[q].ksteps;
-    if (at < rest * cut) {
-      const int j = at / rest;
-      w.which = q, w.index = p.rounds[q] * n_pairs + at - j * rest;
-      w.k_lo = ks * j / cut, w.k_hi = ks * (j + 1) / cut;
-      w.partial = j < cut - 1;
-      w.parts = w.partial ? 0 : j;
-      w.stride = rest;
-      return true;
-    }
-    at -= rest * cut;
+  const int r = i - n0;
+  t.which = 1;
+  if (r < p.rounds1) {
+    t.index = r * n_pairs + pair;
+  } else {
+    if (pair < p.first_light) return false;
+    t.index = p.rounds1 * n_pairs + (r - p.rounds1) * (n_pairs - p.first_light) + pair - p.first_light;
   }
-  return false;
-}
-
-// Bounded wait for another pair's partial sums (acquire).
-RNX_DEVICE bool part_wait(const uint32_t* flag) {
-  const unsigned long long t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-    if (v) return true;
-    if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  }
+  return t.index < p.tiles1;
 }
 
 // Groups of kRaster m tiles, n across: the tiles at work at any time share a
@@ -552,7 +515,15 @@ RNX_DEVICE void box_issue(BoxLoad& b, const uint16_t* src, long long ld, int row
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
     b.v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows && left > 0) b.v[i] = *reinterpret_cast<const uint4*>(src + r * ld + 8 * c);
+    if (r < rows && left >= 8) {
+      b.v[i] = *reinterpret_cast<const uint4*>(src + r * ld + 8 * c);
+    } else if (r < rows && left > 0) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) w[e >> 1] |= (uint32_t)src[r * ld + 8 * c + e] << (16 * (e & 1));
+      b.v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
@@ -615,17 +586,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     Ring r;
     int issued = 0;
     bool ok = true;
-    PairWork t;
-    for (int i = 0; ok && pair_work(p, pair, n_pairs, i, t); ++i) {
+    PairTile t;
+    for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i) {
       const PairProblem& q = p.prob[t.which];
       int mt, nt;
       pair_tile_coords(q, t.index, mt, nt);
       const CUtensorMap* map = is_a ? &q.tma_a : &q.tma_b;
       const int first = is_a ? mt * kPairM + 128 * (int)rank : nt * p.bn + half * (int)rank;   // row of the operand
+      const int ksteps = q.ksteps;
       const bool mn = is_a ? q.a_mn : q.b_mn;
       const bool two = is_a || half > 64;          // MN-major blocks are 64 wide
       const bool expects = is_a && rank == 0;
-      for (int ks = t.k_lo; ks < t.k_hi; ++ks, ++issued, r.next(kPairStages)) {
+      for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
         if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
         if (elect_one()) {
           uint8_t* dst = smem + r.slot * kPairStageBytes + (is_a ? 0 : kABytes);
@@ -654,25 +626,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       Ring r;
       int tc = 0;
       bool ok = true;
-      PairWork t;
-      for (int i = 0; ok && pair_work(p, pair, n_pairs, i, t); ++i, ++tc) {
+      PairTile t;
+      for (int i = 0; ok && pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
         const PairProblem& q = p.prob[t.which];
         const uint32_t idesc = idesc_bf16_major(kPairM, p.bn, q.a_mn, q.b_mn);
         const uint64_t dA0 = q.a_mn ? sdesc_mn_sw128(s0, kMnBlock) : sdesc_k_sw128(s0);
         const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
         const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;
-        const int b = tc & 1;
+        const int b = tc & 1, ksteps = q.ksteps;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u)))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256u * b;
-        for (int ks = t.k_lo; ks < t.k_hi; ++ks, r.next(kPairStages)) {
+        for (int ks = 0; ks < ksteps; ++ks, r.next(kPairStages)) {
           if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t so = (uint64_t)((uint32_t)(r.slot * kPairStageBytes) >> 4);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
-              mma_bf16_pair(acc, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (ks > t.k_lo || kb > 0) ? 1u : 0u);
+              mma_bf16_pair(acc, dA0 + so + kb * stepA, dB0 + so + kb * stepB, idesc, (ks > 0 || kb > 0) ? 1u : 0u);
             mma_commit_pair_mc(&empty_bar[r.slot], 0x3);
           }
           __syncwarp();
@@ -698,10 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* box = smem + (size_t)kPairStages * kPairStageBytes + (size_t)(warp - kFirstEpiWarp) * kEpiBox;
     const int chunks = half / 64;                  // 64-column chunks of this warp
     int tc = 0;
-    PairWork t;
-    const int me = (pair * 2 + (int)rank) * kEpiWarps + warp - kFirstEpiWarp;   // this warp's partial sums and flag
-    const size_t part_floats = (size_t)chunks * 2048;
-    for (int i = 0; pair_work(p, pair, n_pairs, i, t); ++i, ++tc) {
+    PairTile t;
+    for (int i = 0; pair_tile(p, pair, n_pairs, i, t); ++i, ++tc) {
       const PairProblem& q = p.prob[t.which];
       const Epilogue& ep = q.ep;
       int mt, nt;
@@ -714,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(64, q.N - col0);
         BoxLoad res;
         const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
-        if (res_src && ep.vec && !t.partial) box_issue(res, res_src, ep.ldr, rows, cols, lane);
+        if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);
         if (c == 0) {
           if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u) || abort_flag)) {
             gone = true;
@@ -732,36 +702,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(acc_empty_even[b]);
         }
-        if (t.partial) {                           // 512 contiguous bytes per warp and store
-          float4* dst = reinterpret_cast<float4*>(p.parts + me * part_floats + c * 2048) + lane;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            dst[32 * j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                      __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-          if (c == chunks - 1) {
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + me), "r"(1u) : "memory");
-          }
-          continue;
-        }
-        for (int k = 1; k <= t.parts; ++k) {       // the pairs below, nearest first
-          const int other = me - k * t.stride * 2 * kEpiWarps;
-          if (c == 0 && __any_sync(0xffffffffu, !part_wait(p.flags + other))) {
-            gone = true;
-            break;
-          }
-          const float4* src = reinterpret_cast<const float4*>(p.parts + other * part_floats + c * 2048) + lane;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 f = src[32 * j];
-            v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
-            v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
-            v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
-            v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
-          }
-        }
-        if (gone) break;
         if (rows <= 0 || cols <= 0) continue;
         if (ep.bias) {
 #pragma unroll
@@ -953,12 +893,12 @@ struct PackJob {
 struct PackParams {
   PackJob job[2];
   int n;
-  uint32_t* clear;     // status word, where the pack is the call's first launch
+  uint32_t* clear;     // status word (the pack is the call's first launch)
 };
 __global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
   pdl_wait();
   pdl_trigger();
-  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
   for (int q = 0; q < p.n; ++q) {
     const PackJob& d = p.job[q];
     const int groups = (d.cols + 7) / 8;
@@ -1091,83 +1031,33 @@ SplitPlan plan_split(const Product* prod, int n) {
   return best;
 }
 
-// The pair kernel: a round takes the longer of its products and its epilogue; a
-// cut tile also its partial sums, written and read.
-struct PairPlan {
-  double us;
-  int bn;              // 0: none
-  int rounds[2], cut[2], pairs;
-};
-PairPlan plan_pair(const Product* prod, int n, int bn) {
-  constexpr int kPairs = kNumSMs / 2;
-  const double step_us = bn == 256 ? 0.28 : 0.195, epi_us = bn == 256 ? 2.4 : 1.4;
-  PairPlan q{};
-  q.bn = bn;
-  q.us = (bn == 256 ? 8.1 : 6.5) - 0.5;
-  q.cut[0] = q.cut[1] = 1;
-  long long rest[2] = {0, 0}, steps[2] = {0, 0};
+// A round of the pair kernel takes the longer of its products and its epilogue.
+double pair_us(const Product* prod, int n, int bn) {
+  long long tiles = 0;
+  double sum = 0;
   for (int i = 0; i < n; ++i) {
-    const long long tiles = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
-    steps[i] = ceil_div(prod[i].red, kStepK);
-    q.rounds[i] = (int)(tiles / kPairs);
-    rest[i] = tiles % kPairs;
-    q.us += q.rounds[i] * (std::max(steps[i] * step_us, epi_us) + 0.5);
+    const long long t = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
+    const double steps = (double)ceil_div(prod[i].red, kStepK);
+    sum += t * std::max(steps * (bn == 256 ? 0.28 : 0.195), bn == 256 ? 2.4 : 1.4);
+    tiles += t;
   }
-  auto piece_us = [&](int i, int cut) {
-    return rest[i] ? std::max(ceil_div(steps[i], cut) * step_us, epi_us) + (cut > 1 ? 1.8 + 1.2 * cut : 0.0) : 0.0;
-  };
-  double last = rest[0] + rest[1] > kPairs ? piece_us(0, 1) + piece_us(1, 1) : std::max(piece_us(0, 1), piece_us(1, 1));
-  for (int c0 = 1; c0 <= kMaxCut; ++c0)
-    for (int c1 = 1; c1 <= (rest[1] ? kMaxCut : 1); ++c1) {
-      if (c0 * c1 == 1 || rest[0] * c0 + rest[1] * c1 > kPairs || (c0 > 1 && !rest[0])) continue;
-      if (c0 > steps[0] || (rest[1] && c1 > steps[1])) continue;          // a step per piece at least
-      const double us = std::max(piece_us(0, c0), piece_us(1, c1));
-      if (us < last) last = us, q.cut[0] = c0, q.cut[1] = c1;
-    }
-  q.us += last + (last > 0 ? 0.5 : 0.0);
-  q.pairs = q.rounds[0] + q.rounds[1] ? kPairs : (int)std::min<long long>(kPairs, rest[0] * q.cut[0] + rest[1] * q.cut[1]);
-  return q;
+  const long long rounds = ceil_div(tiles, kNumSMs / 2);
+  return (bn == 256 ? 8.1 : 6.5) + rounds * (sum / tiles) + 0.5 * (rounds - 1);
 }
 
 struct Choice {
   double us;
-  PairPlan pair;       // bn 0: the split kernel
+  int width;           // of the pair kernel's tiles, 0 for the split kernel
   SplitPlan split;
 };
 Choice choose(const Product* prod, int n) {
-  Choice c{0, PairPlan{}, plan_split(prod, n)};
+  Choice c{0, 0, plan_split(prod, n)};
   c.us = c.split.us;
   for (int bn = 128; bn <= 256; bn *= 2) {
-    const PairPlan q = plan_pair(prod, n, bn);
-    if (q.us < c.us) c.us = q.us, c.pair = q;
+    const double us = pair_us(prod, n, bn);
+    if (us < c.us) c.us = us, c.width = bn;
   }
   return c;
-}
-size_t parts_bytes(const Choice& c) {
-  return c.pair.bn && c.pair.cut[0] * c.pair.cut[1] > 1 ? 4 * (size_t)c.pair.pairs * kPairM * c.pair.bn : 0;
-}
-constexpr size_t kFlagBytes = 4 * (size_t)(kNumSMs / 2) * 2 * kEpiWarps;
-
-// The two products of the backward pass, the longer reduction first.
-int backward_products(const Product& dx, bool has_dx, const Product& dw, bool has_dw, Product* prod) {
-  int n = 0;
-  if (has_dx) prod[n++] = dx;
-  if (has_dw) prod[n++] = dw;
-  if (n == 2 && prod[0].red < prod[1].red) std::swap(prod[0], prod[1]);
-  return n;
-}
-// ... in one launch, or one launch each where one wants the other kernel.
-struct BackwardChoice {
-  bool apart;
-  Choice c[2];
-};
-BackwardChoice choose_backward(const Product* prod, int n) {
-  BackwardChoice b{false, {choose(prod, n), Choice{}}};
-  if (n == 2) {
-    const Choice first = choose(prod, 1), second = choose(prod + 1, 1);
-    if (!first.pair.bn != !second.pair.bn && first.us + second.us < b.c[0].us) b = BackwardChoice{true, {first, second}};
-  }
-  return b;
 }
 
 // The products' columns are the split kernel's m side, their rows its j side.
@@ -1227,12 +1117,12 @@ cudaError_t launch_pair_act(const PairParams& p, int pairs, cudaStream_t st) {
   return launch_pdl(linear_pair_kernel<ACT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, p);
 }
 
-// parts, flags: of a plan with cut tiles.
-cudaError_t launch_pair(int act, const Product* prod, int n, const PairPlan& plan, const DbJoin& db, uint32_t* status,
-                        float* parts, uint32_t* flags, bool clear, cudaStream_t st) {
+cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoin& db, uint32_t* status, bool clear,
+                        cudaStream_t st) {
   PairParams p;
   memset(&p, 0, sizeof p);
-  const int bn = plan.bn, pairs = plan.pairs;
+  constexpr int kPairs = kNumSMs / 2;
+  long long tiles[2] = {0, 0};
   for (int i = 0; i < n; ++i) {
     PairProblem& q = p.prob[i];
     q.M = prod[i].a.rows;
@@ -1243,11 +1133,8 @@ cudaError_t launch_pair(int act, const Product* prod, int n, const PairPlan& pla
     q.mt = (q.M + kPairM - 1) / kPairM;
     q.nt = (q.N + bn - 1) / bn;
     q.ep = prod[i].ep;
-    // a tensor store writes whole 16-byte pieces: past the last column of an N
-    // that is no multiple of 8 it left its box's values in the row's padding
-    q.ep.vec = q.ep.vec && q.N % 8 == 0;
-    if ((long long)q.mt * q.nt > 1 << 30) return cudaErrorInvalidValue;
-    p.tiles[i] = q.mt * q.nt;
+    tiles[i] = (long long)q.mt * q.nt;
+    if (tiles[i] > 1 << 30) return cudaErrorInvalidValue;
     if (!operand_map(&q.tma_a, prod[i].a, prod[i].red, kTileM) || !operand_map(&q.tma_b, prod[i].b, prod[i].red, bn / 2))
       return cudaErrorInvalidValue;
     auto out_map = [&](CUtensorMap* m, const uint16_t* out, long long ld) {
@@ -1256,16 +1143,28 @@ cudaError_t launch_pair(int act, const Product* prod, int n, const PairPlan& pla
     };
     if (q.ep.vec && (!out_map(&q.tma_out, q.ep.out, q.ep.ldo) || (q.ep.z && !out_map(&q.tma_z, q.ep.z, q.ep.ldz))))
       return cudaErrorInvalidValue;
-    p.rounds[i] = plan.rounds[i];
   }
-  p.cut[0] = plan.cut[0];
-  p.cut[1] = plan.cut[1];
+  p.tiles0 = (int)tiles[0];
+  p.tiles1 = (int)tiles[1];
   p.bn = bn;
   p.db = db;
   p.status = status;
-  p.parts = parts;
-  p.flags = flags;
   p.clear = clear;
+  const int pairs = (int)std::min<long long>(kPairs, std::max<long long>(tiles[0], tiles[1]));
+  // second product: how many rounds all pairs share before those with a tile
+  // less of the first product go on alone, for the earliest end
+  const long long each = p.tiles0 / pairs, heavy = p.tiles0 % pairs;
+  const long long k0 = p.prob[0].ksteps, k1 = p.prob[1].ksteps;
+  p.first_light = (int)heavy;
+  long long best = -1;
+  for (long long q = 0; q <= (tiles[1] + pairs - 1) / pairs; ++q) {
+    const long long rest = std::max<long long>(0, tiles[1] - q * pairs), light = pairs - heavy;
+    const long long end = std::max((each + (heavy > 0)) * k0 + q * k1, each * k0 + (q + (rest + light - 1) / light) * k1);
+    if (best < 0 || end < best) {
+      best = end;
+      p.rounds1 = (int)q;
+    }
+  }
   switch (act) {
     case MOE_ACT_NONE: return launch_pair_act<MOE_ACT_NONE>(p, pairs, st);
     case MOE_ACT_RELU: return launch_pair_act<MOE_ACT_RELU>(p, pairs, st);
@@ -1315,60 +1214,25 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-namespace {
-
-// Status word, the flags of a plan with cut tiles right behind it (one memset
-// clears both), copies of x and w where their pitch asks for them.
-size_t head_layout(LinearLayout& L, bool cuts, int T, int K, int N, long long ldx, long long ldw) {
-  size_t o = 256;
-  L.flags = o;
-  if (cuts) o = up256(o + kFlagBytes);
+LinearLayout linear_layout(int T, int K, int N, long long ldx, long long ldw) {
+  LinearLayout L{};
+  size_t o = 256;                                             // status word
   L.x = o;
   if (needs_copy(T, ldx)) o = up256(o + 2 * (size_t)T * up8(K));
   L.w = o;
   if (needs_copy(N, ldw)) o = up256(o + 2 * (size_t)N * up8(K));
-  return o;
-}
-
-Product forward_product(const Operand& x, const Operand& w, int K, const Epilogue& ep) { return Product{x, w, K, ep}; }
-Product dx_product(const Operand& dz, const Operand& w, int N, const Epilogue& ep) { return Product{dz, w, N, ep}; }
-Product dw_product(const Operand& dzt, const Operand& xt, int T, const Epilogue& ep) { return Product{dzt, xt, T, ep}; }
-
-}  // namespace
-
-LinearLayout linear_layout(int T, int K, int N, long long ldx, long long ldw) {
-  LinearLayout L{};
-  size_t parts = 0;
-  if (T > 0) {
-    const Product q = forward_product(Operand{nullptr, 0, T, false}, Operand{nullptr, 0, N, false}, K, Epilogue{});
-    parts = parts_bytes(choose(&q, 1));
-  }
-  L.parts = L.dz = L.db = head_layout(L, parts > 0, T, K, N, ldx, ldw);
-  L.bytes = up256(L.parts + parts);
+  L.dz = L.part = L.bytes = o;
   return L;
 }
 
 LinearLayout linear_backward_layout(int T, int K, int N, long long ldx, long long ldw) {
-  LinearLayout L{};
-  size_t parts = 0;
-  if (T > 0) {
-    // whichever of dx and dw a call asks for
-    const Product dx = dx_product(Operand{nullptr, 0, T, false}, Operand{nullptr, 0, K, true}, N, Epilogue{});
-    const Product dw = dw_product(Operand{nullptr, 0, N, true}, Operand{nullptr, 0, K, true}, T, Epilogue{});
-    for (int ask = 1; ask <= 3; ++ask) {
-      Product prod[2];
-      const int n = backward_products(dx, ask & 1, dw, ask & 2, prod);
-      const BackwardChoice b = choose_backward(prod, n);
-      for (int i = 0; i <= b.apart; ++i) parts = std::max(parts, parts_bytes(b.c[i]));
-    }
-  }
-  size_t o = head_layout(L, parts > 0, T, K, N, ldx, ldw);
+  LinearLayout L = linear_layout(T, K, N, ldx, ldw);
+  size_t o = L.bytes;
   L.dz = o;
   o = up256(o + 2 * (size_t)T * up8(N));
-  L.db = o;
+  L.part = o;
   if (T > 0) o = up256(o + 4 * (size_t)N * ((T + dz_rows(T, N) - 1) / dz_rows(T, N)));
-  L.parts = o;
-  L.bytes = up256(o + parts);
+  L.bytes = o;
   return L;
 }
 
@@ -1385,24 +1249,16 @@ cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t s
     w = Operand{reinterpret_cast<uint16_t*>(base + L.w), up8(a.K), a.N, false};
     pk.job[pk.n++] = PackJob{a.w, reinterpret_cast<uint16_t*>(base + L.w), a.ldw, w.ld, a.N, a.K};
   }
-  uint32_t* status = reinterpret_cast<uint32_t*>(base);
+  pk.clear = reinterpret_cast<uint32_t*>(base);
+  cudaError_t e = launch_pack(pk, st);
+  if (e != cudaSuccess) return e;
   Epilogue ep{a.bias, a.residual, a.z, a.y, a.ldr, a.ldz, a.ldy, 0};
   ep.vec = vec_ok(ep);
-  const Product prod = forward_product(x, w, a.K, ep);
+  const Product prod{x, w, a.K, ep};
+  uint32_t* status = reinterpret_cast<uint32_t*>(base);
   const Choice c = choose(&prod, 1);
-  cudaError_t e;
-  bool clear = true;                   // for the call's first launch
-  if (parts_bytes(c)) {                // status word and flags
-    if ((e = cudaMemsetAsync(base, 0, L.flags + kFlagBytes, st)) != cudaSuccess) return e;
-    clear = false;
-  }
-  pk.clear = clear ? status : nullptr;
-  if ((e = launch_pack(pk, st)) != cudaSuccess) return e;
-  clear = clear && pk.n == 0;
-  if (c.pair.bn)
-    return launch_pair(act, &prod, 1, c.pair, DbJoin{}, status, reinterpret_cast<float*>(base + L.parts),
-                       reinterpret_cast<uint32_t*>(base + L.flags), clear, st);
-  return launch_split(act, &prod, 1, c.split, DbJoin{}, status, clear, st);
+  if (c.width) return launch_pair(act, &prod, 1, c.width, DbJoin{}, status, pk.n == 0, st);
+  return launch_split(act, &prod, 1, c.split, DbJoin{}, status, pk.n == 0, st);
 }
 
 cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* ws, cudaStream_t st) {
@@ -1423,28 +1279,9 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     ldw = up8(a.K);
     pk.job[pk.n++] = PackJob{a.w, reinterpret_cast<uint16_t*>(base + L.w), a.ldw, ldw, a.N, a.K};
   }
-  // dx[t, k] = sum_n dz[t, n] w[n, k];  dw[n, k] = sum_t dz[t, n] x[t, k]
-  auto out = [](uint16_t* p, long long ld) {
-    Epilogue ep{nullptr, nullptr, nullptr, p, 0, 0, ld, 0};
-    ep.vec = vec_ok(ep);
-    return ep;
-  };
-  const Product dx = dx_product(Operand{nullptr, 0, a.T, false}, Operand{w, ldw, a.K, true}, a.N, out(a.dx, a.lddx));
-  const Product dw = dw_product(Operand{nullptr, 0, a.N, true}, Operand{x, ldx, a.K, true}, a.T, out(a.dw, a.lddw));
-  Product prod[2];
-  const int n = backward_products(dx, a.dx != nullptr, dw, a.dw != nullptr, prod);
-  BackwardChoice choice{};
-  bool clear = true;                   // for the call's first launch
-  if (n) {
-    choice = choose_backward(prod, n);
-    if (parts_bytes(choice.c[0]) || parts_bytes(choice.c[1])) {       // status word and flags
-      if ((e = cudaMemsetAsync(base, 0, L.flags + kFlagBytes, st)) != cudaSuccess) return e;
-      clear = false;
-    }
-  }
-  pk.clear = clear ? status : nullptr;
+  pk.clear = status;
   if ((e = launch_pack(pk, st)) != cudaSuccess) return e;
-  clear = clear && pk.n == 0;
+  bool clear = pk.n == 0;              // for the call's first launch
 
   // dz: dy itself where the layer has no activation and dy can be an operand
   const bool products = a.dx || a.dw, write_dz = products && (act != MOE_ACT_NONE || needs_copy(a.T, a.lddy));
@@ -1455,7 +1292,7 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     uint16_t* dst = write_dz ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
     const long long pitch = up8(a.N);
     const int rows = dz_rows(a.T, a.N), chunks = (a.T + rows - 1) / rows;
-    float* part = a.db ? reinterpret_cast<float*>(base + L.db) : nullptr;
+    float* part = a.db ? reinterpret_cast<float*>(base + L.part) : nullptr;
     const dim3 grid((a.N + 255) / 256, chunks);
     const bool vec = a.lddy % 8 == 0 && (act == MOE_ACT_NONE || a.ldz % 8 == 0);
     switch (act) {
@@ -1476,20 +1313,36 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (a.db) db = DbJoin{part, a.db, chunks, a.N};
   }
-  for (int i = 0; i < n; ++i) {        // dz is the A operand of both
-    prod[i].a.p = dz;
-    prod[i].a.ld = lddz;
-  }
-  for (int i = 0; n && i <= choice.apart; ++i) {
-    const Choice& c = choice.c[i];
-    const Product* q = prod + i;
-    const int count = choice.apart ? 1 : n;
-    e = c.pair.bn ? launch_pair(MOE_ACT_NONE, q, count, c.pair, db, status, reinterpret_cast<float*>(base + L.parts),
-                                reinterpret_cast<uint32_t*>(base + L.flags), clear, st)
-                  : launch_split(MOE_ACT_NONE, q, count, c.split, db, status, clear, st);
-    if (e != cudaSuccess) return e;
+  Product prod[2];
+  int n = 0;
+  auto take = [&](uint16_t* out, long long ldo, const Operand& rows, const Operand& cols, int red) {
+    Epilogue ep{nullptr, nullptr, nullptr, out, 0, 0, ldo, 0};
+    ep.vec = vec_ok(ep);
+    prod[n++] = Product{rows, cols, red, ep};
+  };
+  // dx[t, k] = sum_n dz[t, n] w[n, k];  dw[n, k] = sum_t dz[t, n] x[t, k]
+  if (a.dx) take(a.dx, a.lddx, Operand{dz, lddz, a.T, false}, Operand{w, ldw, a.K, true}, a.N);
+  if (a.dw) take(a.dw, a.lddw, Operand{dz, lddz, a.N, true}, Operand{x, ldx, a.K, true}, a.T);
+  if (n == 2 && prod[0].red < prod[1].red) std::swap(prod[0], prod[1]);   // the longer tiles first
+  auto launch = [&](const Product* q, int count, const Choice& c) {
+    const cudaError_t err = c.width ? launch_pair(MOE_ACT_NONE, q, count, c.width, db, status, clear, st)
+                                    : launch_split(MOE_ACT_NONE, q, count, c.split, db, status, clear, st);
     db = DbJoin{};
     clear = false;
+    return err;
+  };
+  if (n) {
+    // both in one launch, or one launch each where one wants the other kernel
+    const Choice both = choose(prod, n);
+    if (n == 2) {
+      const Choice first = choose(prod, 1), second = choose(prod + 1, 1);
+      if (!first.width != !second.width && first.us + second.us < both.us) {
+        if ((e = launch(prod, 1, first)) != cudaSuccess) return e;
+        if ((e = launch(prod + 1, 1, second)) != cudaSuccess) return e;
+        n = 0;
+      }
+    }
+    if (n && (e = launch(prod, n, both)) != cudaSuccess) return e;
   }
   if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);
   return cudaSuccess;
