@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // Warps: 0 and 3 = TMA producers of A and of B, 1 = MMA issuer (even CTA), 2 =
 // TMEM allocator, then db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
 // 64 columns at a time go through a swizzled 32-row box in shared memory, from
-// which one tensor store writes them (2-byte stores where the pitch is no
-// multiple of 16 bytes).
+// which one tensor store writes them (2-byte stores where the pitch or N is no
+// multiple of 8 elements).
 // Every wait is bounded. No TMA load uses cluster multicast.
 
 constexpr int kPairM = 256;
@@ -416,7 +416,7 @@ static_assert(kPairSmem <= kMaxDynamicSmem, "shared memory");
 
 struct PairProblem {
   CUtensorMap tma_a, tma_b;
-  CUtensorMap tma_out, tma_z;  // of the output and z where their rows allow it (ep.vec): box 64 x 32 rows
+  CUtensorMap tma_out, tma_z;  // of the output and z where rows and N allow it (ep.vec): box 64 x 32 rows
   Epilogue ep;
   int M, N;
   int ksteps;
@@ -515,15 +515,7 @@ RNX_DEVICE void box_issue(BoxLoad& b, const uint16_t* src, long long ld, int row
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
     b.v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows && left >= 8) {
-      b.v[i] = *reinterpret_cast<const uint4*>(src + r * ld + 8 * c);
-    } else if (r < rows && left > 0) {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < left) w[e >> 1] |= (uint32_t)src[r * ld + 8 * c + e] << (16 * (e & 1));
-      b.v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if (r < rows && left > 0) b.v[i] = *reinterpret_cast<const uint4*>(src + r * ld + 8 * c);
   }
 }
 RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
@@ -973,10 +965,11 @@ cudaError_t launch_split_act(const SplitParams& p, int smem, cudaStream_t st) {
 // ---------------------------------------------------------------- choice of kernel and tiles
 // Estimated times in microseconds at 1.9 GHz, fitted to 90 measured
 // combinations of shape (1 to 5000 tokens, 256 to 12288 features), tile width
-// and split; the choices by them took 0.6% longer on average than the best
-// measured ones. What they weigh: narrow tiles and deep splits use more SMs
-// but stream A more often and fill more than one wave; the pair kernel reads
-// least and overlaps its epilogue but needs many tiles.
+// and split. On 32 random shapes of up to 3000 tokens the choices by them took
+// 1.5% longer on average, 24% at most, than the best of the forms measured.
+// What they weigh: narrow tiles and deep splits use more SMs but stream A more
+// often and fill more than one wave; the pair kernel reads least and overlaps
+// its epilogue but needs many tiles.
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -1015,11 +1008,13 @@ SplitPlan plan_split(const Product* prod, int n) {
     for (int S = 1; S <= kMaxSplit; S *= 2) {
       const int cap = split_capacity(two, S);
       const bool shared = two && tiles * S > kNumSMs;        // two CTAs share an SM's bandwidth
+      const double busy = std::min(1.0, (double)tiles * S / kNumSMs);
+      const double kb_us = two ? (shared ? 0.0225 : 0.0126) : 0.0085 + 0.0021 * busy;
       double longest = 0, sum = 0;
       for (int i = 0; i < n; ++i) {
         const long long t = ceil_div(prod[i].b.rows, kTileM) * ceil_div(prod[i].a.rows, bn[i]);
         const double kb = 16 + bn[i] / 8.0, steps = (double)ceil_div(ceil_div(prod[i].red, kStepK), S);
-        const double us = steps * kb * (two ? (shared ? 0.0174 : 0.0126) : 0.0091) + 0.0196 * bn[i] + 0.0197 * bn[i] / S + 2.85;
+        const double us = steps * kb * kb_us + 0.0196 * bn[i] + 0.0197 * bn[i] / S + 2.85;
         longest = std::max(longest, us);
         sum += us * t / tiles;
       }
@@ -1031,17 +1026,19 @@ SplitPlan plan_split(const Product* prod, int n) {
   return best;
 }
 
-// A round of the pair kernel takes the longer of its products and its epilogue.
+// A round of the pair kernel takes the longer of its products and its epilogue;
+// a step takes longer the more pairs are at work (L2 and power).
 double pair_us(const Product* prod, int n, int bn) {
+  constexpr int kPairs = kNumSMs / 2;
   long long tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
+  const long long rounds = ceil_div(tiles, kPairs);
+  const double busy = (double)tiles / (rounds * kPairs);
+  const double step_us = bn == 256 ? 0.28 + 0.09 * busy : 0.215 + 0.05 * busy;
   double sum = 0;
-  for (int i = 0; i < n; ++i) {
-    const long long t = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
-    const double steps = (double)ceil_div(prod[i].red, kStepK);
-    sum += t * std::max(steps * (bn == 256 ? 0.28 : 0.195), bn == 256 ? 2.4 : 1.4);
-    tiles += t;
-  }
-  const long long rounds = ceil_div(tiles, kNumSMs / 2);
+  for (int i = 0; i < n; ++i)
+    sum += (double)(ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn)) *
+           std::max(ceil_div(prod[i].red, kStepK) * step_us, bn == 256 ? 2.4 : 1.4);
   return (bn == 256 ? 8.1 : 6.5) + rounds * (sum / tiles) + 0.5 * (rounds - 1);
 }
 
@@ -1133,6 +1130,9 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
     q.mt = (q.M + kPairM - 1) / kPairM;
     q.nt = (q.N + bn - 1) / bn;
     q.ep = prod[i].ep;
+    // a tensor store writes whole 16-byte pieces: past the last column of an N
+    // that is no multiple of 8 it left its box's values in the row's padding
+    q.ep.vec = q.ep.vec && q.N % 8 == 0;
     tiles[i] = (long long)q.mt * q.nt;
     if (tiles[i] > 1 << 30) return cudaErrorInvalidValue;
     if (!operand_map(&q.tma_a, prod[i].a, prod[i].red, kTileM) || !operand_map(&q.tma_b, prod[i].b, prod[i].red, bn / 2))

@@ -139,9 +139,9 @@ RNX_DEVICE void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uin
       : "memory");
 }
 
-// Ask L2 for the box at (x, y); no completion to wait for.
-RNX_DEVICE void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+// Bring a tensor map (a kernel parameter) into the copy engine's cache.
+RNX_DEVICE void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // 2D tiled store of the box at (x, y) from shared memory (the layout the

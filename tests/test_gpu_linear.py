@@ -104,6 +104,10 @@ SHAPES = [
     (2049, 4096, 1280, "silu", True, True, True, None),
     (5000, 64, 129, "none", False, True, False, None),
     (4096, 1024, 4096, "gelu", True, False, True, (16, 8, 24)),
+    # long reductions, a padded pitch under an odd length
+    (600, 12288, 1024, "gelu", True, True, True, None),
+    (1300, 6000, 1101, "silu", True, True, True, (0, 0, 3)),
+    (300, 4096, 6000, "none", False, True, False, None),
 ]
 
 
@@ -202,6 +206,9 @@ def _check_backward(T, K, N, act, x, w, z, g, want=("dx", "dw", "db"), pitches=N
     (2048, 1024, 1536, "gelu", ("dx", "dw", "db"), None),
     (1025, 2048, 512, "none", ("dx", "dw", "db"), (16, 8, 8)),
     (6000, 64, 128, "relu", ("dx", "dw", "db"), None),
+    (2500, 2000, 1100, "gelu", ("dx", "dw", "db"), None),
+    (1200, 4100, 2000, "none", ("dx", "dw"), None),
+    (1300, 2050, 4500, "silu", ("dx",), (3, 5, 0)),
 ])
 def test_backward_matches_the_formula(T, K, N, act, want, pitches):
     g = torch.Generator().manual_seed(T + K + N)
@@ -248,7 +255,7 @@ def test_no_tokens():
     assert not buf[:, :64].any() and not db.any() and bool((buf[:, 64:] == 77.0).all())
 
 
-@pytest.mark.parametrize("T,K,N", [(6, 512, 640), (700, 515, 333)])
+@pytest.mark.parametrize("T,K,N", [(6, 512, 640), (700, 515, 333), (2049, 1032, 4096)])
 def test_repeats_graphs_and_streams(T, K, N):
     g = torch.Generator().manual_seed(4)
     data = [(_rand(g, T, K), _rand(g, T, N, scale=0.1)) for _ in range(2)]
@@ -305,6 +312,27 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
     for x, w, y, ws, _ in jobs:
         capi.moe_read_device_status(ws)
         _check_forward(x, w, None, None, y, None, "silu")
+
+
+def test_two_large_calls_at_once():
+    """Two launches that each fill the GPU, competing for the SMs."""
+    g = torch.Generator().manual_seed(8)
+    jobs = []
+    for T, K, N in ((2049, 4096, 1280), (700, 8192, 4000)):
+        x, w = _rand(g, T, K), _rand(g, N, K, scale=K ** -0.5)
+        y = [torch.empty(T, N, dtype=BF16, device="cuda") for _ in range(2)]
+        ws = capi.alloc_linear_workspace(x, w)
+        capi.linear_bf16(x, w, y[0], ws, act="silu")
+        jobs.append((x, w, y, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for x, w, y, ws, st in jobs:
+            capi.linear_bf16(x, w, y[1], ws, act="silu", stream=st)
+    torch.cuda.synchronize()
+    for x, w, y, ws, _ in jobs:
+        capi.moe_read_device_status(ws)
+        assert torch.equal(y[0], y[1])
+        _check_forward(x, w, None, None, y[1], None, "silu")
 
 
 def test_a_training_block_with_the_router():
