@@ -186,7 +186,12 @@ RNX_DEVICE void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// 16 bytes of fp32 from a peer CTA's shared memory (a shared::cluster address).
+// The same without ordering memory: every thread of the cluster has arrived.
+RNX_DEVICE void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// fp32 from a CTA of the cluster (shared::cluster address).
 RNX_DEVICE float4 ld_cluster_f4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -195,11 +200,18 @@ RNX_DEVICE float4 ld_cluster_f4(uint32_t cluster_addr) {
                : "memory");
   return v;
 }
-
 RNX_DEVICE float ld_cluster_f1(uint32_t cluster_addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
   return v;
+}
+
+// Store one word into a CTA of the cluster; its 4 bytes are counted on the
+// barrier (shared::cluster addresses of the same CTA).
+RNX_DEVICE void st_async(uint32_t cluster_addr, uint32_t v, uint32_t bar_cluster) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
+               "r"(bar_cluster)
+               : "memory");
 }
 
 RNX_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
