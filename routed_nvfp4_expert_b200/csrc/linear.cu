@@ -132,7 +132,8 @@ struct Epilogue {
   int vec;                    // rows of residual, z and out all start on 16-byte boundaries
 };
 
-// db from the column sums of the row chunks, in chunk order, by one warp per CTA.
+// db from the column sums of the row chunks, by one warp per CTA: four lanes
+// per column take every fourth chunk in order, then add theirs.
 struct DbJoin {
   const float* part;          // [chunks, n]
   float* db;                  // nullable
@@ -140,11 +141,16 @@ struct DbJoin {
 };
 RNX_DEVICE void join_db(const DbJoin& d, int cta, int ctas, int lane) {
   if (!d.db) return;
-  for (int c = cta * 32 + lane; c < d.n; c += ctas * 32) {
+  for (int c0 = cta * 8; c0 < d.n; c0 += ctas * 8) {        // warp-uniform
+    const int c = c0 + lane / 4;
     float v = 0.f;
+    if (c < d.n) {
 #pragma unroll 8
-    for (int i = 0; i < d.chunks; ++i) v += d.part[(size_t)i * d.n + c];
-    d.db[c] = v;
+      for (int i = lane % 4; i < d.chunks; i += 4) v += d.part[(size_t)i * d.n + c];
+    }
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    if (c < d.n && lane % 4 == 0) d.db[c] = v;
   }
 }
 
@@ -916,22 +922,22 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
-  for (int q = 0; q < p.n; ++q) {
-    const PackJob& d = p.job[q];
+  const long long first = p.job[0].rows * (long long)((p.job[0].cols + 7) / 8);
+  const long long items = first + (p.n > 1 ? p.job[1].rows * (long long)((p.job[1].cols + 7) / 8) : 0);
+  for (long long at = (long long)blockIdx.x * 256 + threadIdx.x; at < items; at += (long long)gridDim.x * 256) {
+    const PackJob& d = p.job[at >= first];
+    const long long i = at >= first ? at - first : at;
     const int groups = (d.cols + 7) / 8;
-    const long long items = (long long)d.rows * groups;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
-      const long long r = i / groups;
-      const int c = 8 * (int)(i - r * groups);
-      const uint16_t* s = d.src + r * d.ld_src + c;
-      uint32_t w[4];
+    const long long r = i / groups;
+    const int c = 8 * (int)(i - r * groups);
+    const uint16_t* s = d.src + r * d.ld_src + c;
+    uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = c + 2 * k < d.cols ? s[2 * k] : 0u, hi = c + 2 * k + 1 < d.cols ? s[2 * k + 1] : 0u;
-        w[k] = lo | (hi << 16);
-      }
-      *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = c + 2 * k < d.cols ? s[2 * k] : 0u, hi = c + 2 * k + 1 < d.cols ? s[2 * k + 1] : 0u;
+      w[k] = lo | (hi << 16);
     }
+    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -1213,8 +1219,8 @@ long long operand_pitch(int rows, long long ld) { return rows > 1 ? ld : up8(ld)
 cudaError_t launch_pack(const PackParams& p, cudaStream_t st) {
   if (p.n == 0) return cudaSuccess;
   long long items = 0;
-  for (int i = 0; i < p.n; ++i) items = std::max(items, (long long)p.job[i].rows * ((p.job[i].cols + 7) / 8));
-  const int grid = (int)std::min<long long>((items + 255) / 256, 8 * kNumSMs);
+  for (int i = 0; i < p.n; ++i) items += (long long)p.job[i].rows * ((p.job[i].cols + 7) / 8);
+  const int grid = (int)std::min<long long>((items + 255) / 256, 16 * kNumSMs);
   return launch_pdl(pack_rows_kernel, dim3(grid), dim3(256), 0, st, p);
 }
 
@@ -1228,10 +1234,10 @@ cudaError_t launch_dz(bool vec, dim3 grid, cudaStream_t st, const uint16_t* dy, 
 }
 
 // Rows per CTA of the dz pass: one round of loads, more where that gives over
-// eight CTAs per SM.
+// eight CTAs per SM or more than 128 chunks for db's join.
 int dz_rows(int T, int N) {
-  const long long round = 8 * kDzRows, strips = (N + 255) / 256;
-  const long long rounds = ((T + round - 1) / round * strips + 8 * kNumSMs - 1) / (8 * kNumSMs);
+  const long long round = 8 * kDzRows, strips = (N + 255) / 256, all = (T + round - 1) / round;
+  const long long rounds = std::max((all * strips + 8 * kNumSMs - 1) / (8 * kNumSMs), (all + 127) / 128);
   return (int)(round * rounds);
 }
 
@@ -1369,7 +1375,7 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (n && (e = launch(prod, n, both)) != cudaSuccess) return e;
   }
-  if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);
+  if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 7) / 8), dim3(32), 0, st, db);
   return cudaSuccess;
 }
 
