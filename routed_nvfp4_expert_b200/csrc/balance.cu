@@ -13,9 +13,9 @@
 // and d l = d s * s (1 - s).
 //
 // Both directions are streams over the logits [T, E] (4 T E bytes forward, 8 T
-// E backward). A row is held in registers by G lanes (8 up to E = 320), four
-// consecutive logits each, so a warp works on 32 / G rows at a time and the
-// row's sums cost 3 shuffles for four rows: with a whole warp per row the
+// E backward). A row is held in registers by G lanes (4 up to E = 32, 8 up to 320),
+// four consecutive logits each, so a warp works on 32 / G rows at a time and
+// at E = 288 the row's sums cost 3 shuffles for four rows: with a whole warp per row the
 // shuffles, the slot loop and the bookkeeping of each row took as many issue
 // slots as its 288 logits (42 us forward at 131072 x 288, 46 us backward at
 // 65536 x 288).
@@ -28,8 +28,9 @@ namespace rnx {
 namespace {
 
 constexpr int kMaxK = 16;
-constexpr int kSumWarps = 16;          // forward: one 512-thread CTA per SM
-constexpr int kGradWarps = 8;
+// Sixteen warps per SM: one CTA forward, two backward. (Twelve with rings of
+// three rows instead of two: 39.6 against 38.2 us forward at 131072 x 288.)
+constexpr int kSumWarps = 16, kGradWarps = 8;
 constexpr int kJoinWarps = 32;
 // Up to these many tokens a whole warp takes a row: 2.8 against 3.5 us forward
 // at one token of 288 experts, 3.8 against 5.7 us backward at 1024 (one row per
@@ -58,12 +59,20 @@ RNX_DEVICE int seq_start(const int32_t* off, int b, int T) {
   return min(max(*(off + b), 0), T);
 }
 
-// First sequence that ends behind `row` (B if none).
+// First sequence that ends behind `row` (B if none), found by a whole warp (row
+// the same in all lanes): 32 probes at a time, so that up to 32 sequences take
+// one load's latency and 1024 two.
 RNX_DEVICE int seq_of_row(const int32_t* off, int B, int T, int row) {
-  int lo = 0, hi = B;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;                              // the answer is in [lo, hi]
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_start(off, mid + 1, T) > row) hi = mid; else lo = mid + 1;
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;   // the last of the lane's run
+    const bool behind = at >= hi || seq_start(off, at + 1, T) > row;
+    const unsigned hit = __ballot_sync(0xffffffffu, behind);
+    if (hit == 0) return hi;
+    const int i = __ffs(hit) - 1;
+    hi = min(hi, lo + (i + 1) * step - 1);
+    lo += i * step;
   }
   return lo;
 }
@@ -79,8 +88,8 @@ RNX_DEVICE float row_sum(float v) {
 // Rows reach the registers through a ring of slots in shared memory, filled by
 // cp.async DEPTH - 1 rows ahead (74 KB in flight per SM at E = 288, which
 // covers the HBM latency; a second set of registers for the next row spilled).
-// A slot is E logits rounded up to 4, then 16 ids and 16 routing-weight
-// gradients. Lane g of a row takes logits 4 (g + G q) + i; those behind the
+// A slot is E logits rounded up to 4, then 16 ids and, backward, 16
+// routing-weight gradients. Lane g of a row takes logits 4 (g + G q) + i; those behind the
 // last expert (in the last quad alone, 4 G (NQ - 1) < E) are masked.
 RNX_DEVICE void cp_async16(float* dst, const float* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
@@ -93,9 +102,9 @@ template <int N>
 RNX_DEVICE void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __host__ __device__ constexpr int padded(int E) { return (E + 3) / 4 * 4; }
-__host__ __device__ constexpr int slot_floats(int E) { return padded(E) + 2 * kMaxK; }
-template <int NQ>
-__host__ __device__ constexpr int ring_depth() { return NQ <= 5 ? 4 : 2; }
+__host__ __device__ constexpr int slot_floats(int E, bool weights) { return padded(E) + (weights ? 2 : 1) * kMaxK; }
+template <int G, int NQ>
+__host__ __device__ constexpr int ring_depth() { return NQ > 5 ? 2 : G == 4 ? 3 : 4; }
 
 // Where lane g reads its quad q of a slot: the last quad's lanes behind the
 // last expert read the row's last four again, so that no read leaves the slot.
@@ -133,9 +142,9 @@ RNX_DEVICE void fill_slot(float* slot, const float* logits, const int32_t* ids, 
 template <int G, int NQ>
 RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, int lo, int hi, float* rings,
                          float* warp_sums, int* hist) {
-  constexpr int R = 32 / G, STEP = kSumWarps * R, DEPTH = ring_depth<NQ>();
+  constexpr int R = 32 / G, STEP = kSumWarps * R, DEPTH = ring_depth<G, NQ>();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane % G;
-  const int slot = slot_floats(E);
+  const int slot = slot_floats(E, false);
   float* ring = rings + (size_t)(warp * R + lane / G) * DEPTH * slot;
   for (int e = tid; e < E; e += kSumWarps * 32) hist[e] = 0;
   int base = lo + warp * R;                              // the warp's first row (warp-uniform)
@@ -202,7 +211,7 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
 // Shared memory of a summing CTA: rings, the warps' sums, the counts.
 template <int G, int NQ>
 __host__ __device__ constexpr size_t sum_ring_floats(int E) {
-  return (size_t)kSumWarps * (32 / G) * ring_depth<NQ>() * slot_floats(E);
+  return (size_t)kSumWarps * (32 / G) * ring_depth<G, NQ>() * slot_floats(E, false);
 }
 template <int G, int NQ>
 constexpr size_t sum_smem(int E) { return 4 * (sum_ring_floats<G, NQ>(E) + ((size_t)kSumWarps + 1) * E); }
@@ -339,16 +348,17 @@ struct GradParams {
 };
 
 // G lanes per row, each warp a run of consecutive rows, so that the loads f of
-// its sequence stay in registers. The routing weights' part of a row, k values,
-// is spread over the experts through the row's own slot, read and zeroed by
-// then (testing each expert against k ids cost more instructions than
-// everything else).
+// its sequence stay in registers. The routing weights' part of a row is k
+// values: the row without them goes back to its slot, the slots' lanes add
+// theirs, and the row is stored from there (testing each expert against k ids
+// cost more instructions than everything else).
 template <int G, int NQ>
 __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const GradParams p) {
-  constexpr int R = 32 / G, DEPTH = ring_depth<NQ>();
+  constexpr int R = 32 / G, DEPTH = ring_depth<G, NQ>();
+  constexpr int SL = G >= kMaxK ? 1 : kMaxK / G; // slots per lane: slot j + G h of lane j
   extern __shared__ __align__(16) float dyn[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G;
-  const int E = p.E, k = p.k, slot = slot_floats(p.E), tail = padded(p.E);
+  const int E = p.E, k = p.k, slot = slot_floats(p.E, true), tail = padded(p.E);
   const bool vec = E % 4 == 0;
   float* ring = dyn + (size_t)(warp * R + lane / G) * DEPTH * slot;
   pdl_wait();
@@ -365,8 +375,9 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
   };
 #pragma unroll
   for (int d = 0; d < DEPTH - 1; ++d) fill(d, base + d * R);
-  // this lane group's sequence [start, end); the groups of a warp may be in different ones
-  int b = seq_of_row(p.off, p.B, p.T, min(base + mine, p.T - 1));
+  // this lane group's sequence [start, end), from the warp's first on; the
+  // groups of a warp may be in different ones
+  int b = seq_of_row(p.off, p.B, p.T, base);
   int start = b < p.B ? seq_start(p.off, b, p.T) : p.T, end = b < p.B ? seq_start(p.off, b + 1, p.T) : p.T;
   bool fresh = true;
   float f[4 * NQ], gain = 0.f;
@@ -388,66 +399,85 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
       const float n = (float)(end - start);
       gain = p.d_loss[b] * p.coef / n;
       const float fs = (float)E / ((float)k * n);
+      const int32_t* count = p.counts + (size_t)b * E;
 #pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) {
-        const int c = 4 * (g + G * (i / 4)) + i % 4;
-        f[i] = c < E ? (float)p.counts[(size_t)b * E + c] * fs : 0.f;
+      for (int q = 0; q < NQ; ++q) {
+        const int c = 4 * (g + G * q);
+        int4 v = make_int4(0, 0, 0, 0);
+        if (vec) {
+          if (q < NQ - 1 || c < E) v = *reinterpret_cast<const int4*>(count + c);
+        } else {
+          if (q < NQ - 1 || c < E) v.x = count[c];
+          if (q < NQ - 1 || c + 1 < E) v.y = count[c + 1];
+          if (q < NQ - 1 || c + 2 < E) v.z = count[c + 2];
+          if (q < NQ - 1 || c + 3 < E) v.w = count[c + 3];
+        }
+        f[4 * q] = (float)v.x * fs, f[4 * q + 1] = (float)v.y * fs, f[4 * q + 2] = (float)v.z * fs, f[4 * q + 3] = (float)v.w * fs;
       }
     }
     cp_wait<DEPTH - 1>();
     __syncwarp();
     float* src = ring + at * slot;
-    int id[2] = {-1, -1};                        // G >= 8 lanes cover 16 slots in two
-    float d[2];
+    int id[SL];
+    float d[SL];                                 // a slot's part of d logits
     if (p.d_weights) {
-      float sc[2] = {0.f, 0.f}, v[2] = {0.f, 0.f}, unused;
+      float sc[SL], slope[SL], v[SL], c = 0.f, m = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at_j = g + G * j;
-        if (!inside || at_j >= k) continue;
-        const int e = __float_as_int(src[tail + at_j]);
-        if (e < 0 || e >= E) continue;
-        id[j] = e;
-        v[j] = src[tail + kMaxK + at_j];
-        sc[j] = score_of(src[e], unused);
+      for (int h = 0; h < SL; ++h) {
+        const int j = g + G * h;
+        const int e = inside && j < k ? __float_as_int(src[tail + j]) : -1;
+        id[h] = e >= 0 && e < E ? e : -1;
+        float ex;
+        sc[h] = id[h] >= 0 ? score_of(src[id[h]], ex) : 0.f;
+        slope[h] = id[h] >= 0 ? slope_of(sc[h], ex) : 0.f;
+        v[h] = id[h] >= 0 ? src[tail + kMaxK + j] : 0.f;
+        c += sc[h];
+        m = fmaf(v[h], sc[h], m);
       }
-      const float c = row_sum<G>(sc[0] + sc[1]);
+      c = row_sum<G>(c);
+      m = row_sum<G>(m);
       const float ic = c == 0.f ? 0.f : 1.0f / c;
-      const float m = row_sum<G>(v[0] * sc[0] + v[1] * sc[1]) * ic;
+      m *= ic;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) d[j] = p.rsf * ic * (v[j] - m);
+      for (int h = 0; h < SL; ++h) d[h] = p.rsf * ic * (v[h] - m) * slope[h];
+      // An expert named in several slots gets their sum, in slot order, from
+      // its first. Hardly ever: k ids in k lanes are compared with one match.
+      bool twice = k > G;
+      if (!twice) {
+        const unsigned same = __match_any_sync(0xffffffffu, id[0] >= 0 ? mine << 16 | id[0] : -1 - lane);
+        twice = __any_sync(0xffffffffu, same & (same - 1));
+      }
+      if (twice) {
+        float sum[SL];
+        bool lead[SL];
+#pragma unroll
+        for (int h = 0; h < SL; ++h) sum[h] = 0.f, lead[h] = true;
+        for (int j = 0; j < k; ++j) {
+          int ej = id[0];
+          float dj = d[0];
+#pragma unroll
+          for (int h = 1; h < SL; ++h)
+            if (j / G == h) ej = id[h], dj = d[h];
+          ej = __shfl_sync(0xffffffffu, ej, j % G, G);
+          dj = __shfl_sync(0xffffffffu, dj, j % G, G);
+#pragma unroll
+          for (int h = 0; h < SL; ++h) {
+            sum[h] += ej == id[h] ? dj : 0.f;
+            lead[h] = lead[h] && !(ej == id[h] && j < g + G * h);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < SL; ++h) {
+          d[h] = sum[h];
+          if (!lead[h]) id[h] = -1;
+        }
+      }
     }
     float l[4 * NQ], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const float4 v = *reinterpret_cast<const float4*>(src + cell<G, NQ>(q, g, E));
       l[4 * q] = v.x, l[4 * q + 1] = v.y, l[4 * q + 2] = v.z, l[4 * q + 3] = v.w;
-    }
-    if (p.d_weights) {
-      __syncwarp();                              // the chosen logits have been read
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int c = 4 * (g + G * q);
-        if (q < NQ - 1 || c < E) *reinterpret_cast<float4*>(src + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      // an expert named in several slots gets their sum, in slot order, from its first
-      float sum[2] = {0.f, 0.f};
-      bool lead[2] = {id[0] >= 0, id[1] >= 0};
-      for (int j = 0; j < k; ++j) {
-        const int other = j < G ? id[0] : id[1];
-        const float od = j < G ? d[0] : d[1];
-        const int ej = __shfl_sync(0xffffffffu, other, j % G, G);
-        const float dj = __shfl_sync(0xffffffffu, od, j % G, G);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          sum[h] += ej == id[h] ? dj : 0.f;
-          lead[h] = lead[h] && !(ej == id[h] && j < g + G * h);
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (lead[h]) src[id[h]] = sum[h];
     }
 #pragma unroll
     for (int i = 0; i < 4 * NQ; ++i) {
@@ -461,26 +491,39 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
     dot = row_sum<G>(dot);
     const float inv = total == 0.f ? 0.f : 1.0f / total;
     const float mean = dot * inv, scale = gain * inv;
-    __syncwarp();                                // the spread row is complete
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) l[i] *= scale * (f[i] - mean);
+    if (p.d_weights) {
+      __syncwarp();                              // the slot's logits have been read
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int c = 4 * (g + G * q);
+        if (q < NQ - 1 || c < E) *reinterpret_cast<float4*>(src + c) = make_float4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < SL; ++h)
+        if (id[h] >= 0) src[id[h]] += d[h];
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(src + cell<G, NQ>(q, g, E));
+        l[4 * q] = v.x, l[4 * q + 1] = v.y, l[4 * q + 2] = v.z, l[4 * q + 3] = v.w;
+      }
+    }
     if (inside) {
       float* dst = p.d_logits + (size_t)row * E;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         const int c = 4 * (g + G * q);
         if (q == NQ - 1 && c >= E) break;
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.d_weights) w = *reinterpret_cast<const float4*>(src + c);
-        const float4 o = make_float4(fmaf(scale, f[4 * q] - mean, w.x) * l[4 * q],
-                                     fmaf(scale, f[4 * q + 1] - mean, w.y) * l[4 * q + 1],
-                                     fmaf(scale, f[4 * q + 2] - mean, w.z) * l[4 * q + 2],
-                                     fmaf(scale, f[4 * q + 3] - mean, w.w) * l[4 * q + 3]);
         if (vec) {
-          *reinterpret_cast<float4*>(dst + c) = o;
+          *reinterpret_cast<float4*>(dst + c) = make_float4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
         } else {
-          dst[c] = o.x;
-          if (q < NQ - 1 || c + 1 < E) dst[c + 1] = o.y;
-          if (q < NQ - 1 || c + 2 < E) dst[c + 2] = o.z;
-          if (q < NQ - 1 || c + 3 < E) dst[c + 3] = o.w;
+          dst[c] = l[4 * q];
+          if (q < NQ - 1 || c + 1 < E) dst[c + 1] = l[4 * q + 1];
+          if (q < NQ - 1 || c + 2 < E) dst[c + 2] = l[4 * q + 2];
+          if (q < NQ - 1 || c + 3 < E) dst[c + 3] = l[4 * q + 3];
         }
       }
     }
@@ -513,9 +556,13 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
         RNX_CASE(9, CALL, 16, 9);                                \
         default: CALL(16, 10);                                   \
       }                                                          \
+    } else if ((E) <= 32) {                                      \
+      switch (((E) + 15) / 16) {                                 \
+        RNX_CASE(1, CALL, 4, 1);                                 \
+        default: CALL(4, 2);                                     \
+      }                                                          \
     } else {                                                     \
       switch (((E) + 31) / 32) {                                 \
-        RNX_CASE(1, CALL, 8, 1);                                 \
         RNX_CASE(2, CALL, 8, 2);                                 \
         RNX_CASE(3, CALL, 8, 3);                                 \
         RNX_CASE(4, CALL, 8, 4);                                 \
@@ -546,7 +593,7 @@ cudaError_t launch_grad(GradParams p, cudaStream_t st) {
   const int groups = (p.T + R - 1) / R, warps = kNumSMs * 2 * kGradWarps;
   p.rows_per_warp = R * max(1, (groups + warps - 1) / warps);
   const int rows = kGradWarps * p.rows_per_warp;
-  const size_t smem = (size_t)kGradWarps * R * ring_depth<NQ>() * slot_floats(p.E) * 4;   // at most 100 KB
+  const size_t smem = (size_t)kGradWarps * R * ring_depth<G, NQ>() * slot_floats(p.E, true) * 4;   // at most 102 KB
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = smem > 48 * 1024 ? allow_smem(router_grad_kernel<G, NQ>, done) : cudaSuccess;
   return e != cudaSuccess ? e : launch_pdl(router_grad_kernel<G, NQ>, dim3((p.T + rows - 1) / rows), dim3(kGradWarps * 32), smem, st, p);

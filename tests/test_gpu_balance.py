@@ -100,6 +100,9 @@ CASES = [
     (300, 1024, 16, [0, 1, 2, 150, 299], True, True),
     # expert counts that end inside a row's last vectors, at each number of lanes per row
     (20, 33, 3, None, False, False),
+    (50, 40, 4, [0, 20, 50], False, True),
+    (2100, 112, 12, [0, 700, 2090], True, True),
+    (1900, 10, 3, None, False, True),
     (90, 330, 5, [0, 40, 90], False, False),
     (70, 650, 16, None, True, False),
     (3000, 322, 4, [0, 1000, 2999], False, False),
