@@ -912,6 +912,7 @@ struct PackJob {
   uint16_t* dst;
   long long ld_src, ld_dst;
   int rows, cols;
+  unsigned items;      // 256-column pieces, set by launch_pack
 };
 struct PackParams {
   PackJob job[2];
@@ -922,22 +923,20 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
-  const long long first = p.job[0].rows * (long long)((p.job[0].cols + 7) / 8);
-  const long long items = first + (p.n > 1 ? p.job[1].rows * (long long)((p.job[1].cols + 7) / 8) : 0);
-  for (long long at = (long long)blockIdx.x * 256 + threadIdx.x; at < items; at += (long long)gridDim.x * 256) {
+  // a warp per 256 columns of a row (fewer than 2^31 of those fit the device)
+  const int lane = threadIdx.x & 31;
+  const unsigned first = p.job[0].items, items = first + p.job[1].items;
+  for (unsigned at = blockIdx.x * 8 + (threadIdx.x >> 5); at < items; at += gridDim.x * 8) {
     const PackJob& d = p.job[at >= first];
-    const long long i = at >= first ? at - first : at;
-    const int groups = (d.cols + 7) / 8;
-    const long long r = i / groups;
-    const int c = 8 * (int)(i - r * groups);
+    const unsigned i = at >= first ? at - first : at, chunks = (d.cols + 255) / 256, r = i / chunks;
+    const int c = 256 * (int)(i - r * chunks) + 8 * lane;
+    if (c >= d.cols) continue;
     const uint16_t* s = d.src + r * d.ld_src + c;
-    uint32_t w[4];
+    uint32_t e[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = c + 2 * k < d.cols ? s[2 * k] : 0u, hi = c + 2 * k + 1 < d.cols ? s[2 * k + 1] : 0u;
-      w[k] = lo | (hi << 16);
-    }
-    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 8; ++k) e[k] = c + k < d.cols ? s[k] : 0u;
+    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) =
+        make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
   }
 }
 
@@ -1216,11 +1215,16 @@ long long up8(long long v) { return (v + 7) / 8 * 8; }
 bool needs_copy(int rows, long long ld) { return rows > 1 && ld % 8; }
 long long operand_pitch(int rows, long long ld) { return rows > 1 ? ld : up8(ld); }
 
-cudaError_t launch_pack(const PackParams& p, cudaStream_t st) {
+cudaError_t launch_pack(PackParams p, cudaStream_t st) {
   if (p.n == 0) return cudaSuccess;
   long long items = 0;
-  for (int i = 0; i < p.n; ++i) items += (long long)p.job[i].rows * ((p.job[i].cols + 7) / 8);
-  const int grid = (int)std::min<long long>((items + 255) / 256, 16 * kNumSMs);
+  for (int i = 0; i < p.n; ++i) {
+    const long long n = p.job[i].rows * ceil_div(p.job[i].cols, 256);
+    p.job[i].items = (unsigned)n;
+    items += n;
+  }
+  if (items > 1ll << 31) return cudaErrorInvalidValue;
+  const int grid = (int)std::min<long long>((items + 7) / 8, 16 * kNumSMs);
   return launch_pdl(pack_rows_kernel, dim3(grid), dim3(256), 0, st, p);
 }
 
