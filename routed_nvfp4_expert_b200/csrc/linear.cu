@@ -30,53 +30,70 @@ namespace {
 // ---------------------------------------------------------------- activations
 
 // The forward's epilogue evaluates 2^15 of these per CTA and tile beside the
-// next tile's products, so their instruction count matters: normcdff made the
-// epilogue the longer of the two (60% of the tensor pipe at 4096 x 4096 x
-// 12288). GELU takes erfc from Abramowitz and Stegun 7.1.26 (absolute error
-// 1.5e-7), the others the exponential and division intrinsics; all stay
-// within 2^-20 of |z|, far inside the result's bf16 step.
+// next tile's products, and the dz pass as many as it streams, so their
+// instruction count matters: with normcdff, tanhf, expf and full divisions the
+// epilogue took longer than the products (60% of the tensor pipe at 4096 x 4096
+// x 12288, 82% now) and the dz pass 3.3 times its HBM time. Everything is put
+// on one power of two and one reciprocal (within 2^-22 each); GELU takes erfc
+// from Abramowitz and Stegun 7.1.26 (absolute error 1.5e-7). All stay within
+// 2^-20 of 1 + |z|, far inside a bf16 step. With E = 2^(-v log2 e) and s = 1 /
+// (1 + E), 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0.
+
+RNX_DEVICE float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+RNX_DEVICE float recip(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two values rounded to bf16 in one instruction (lo in the low half).
+RNX_DEVICE uint32_t pack2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// Phi(z), with g = exp(-z^2 / 2): erfc(|z| / sqrt 2) / 2 = g (a polynomial in
+// t = 1 / (1 + 0.3275911 |z| / sqrt 2) with half of 7.1.26's coefficients).
+RNX_DEVICE float normal_cdf(float z, float& g) {
+  const float t = recip(fmaf(0.23164189f, fabsf(z), 1.f));
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
+                              0.127414796f);
+  g = pow2(-0.72134752f * z * z);
+  const float tail = poly * g;
+  return z > 0.f ? 1.f - tail : tail;
+}
+
 template <int ACT>
 RNX_DEVICE float act_of(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if (ACT == MOE_ACT_GELU) {
-    const float x = fabsf(z) * 0.7071067811865476f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    const float tail = 0.5f * poly * __expf(-x * x);      // 1 - Phi(|z|)
-    return z * (z > 0.f ? 1.f - tail : tail);
+    float g;
+    return z * normal_cdf(z, g);
   }
-  if (ACT == MOE_ACT_GELU_TANH) {                          // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-    const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
-    return __fdividef(z, 1.f + __expf(-u2));
-  }
-  if (ACT == MOE_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  // (1 + tanh u) / 2 = 1 / (1 + e^-2u), 2 u log2 e = z (2.3022082 + 0.10294325 z^2)
+  if (ACT == MOE_ACT_GELU_TANH) return z * recip(1.f + pow2(z * fmaf(-0.10294325f * z, z, -2.3022082f)));
+  if (ACT == MOE_ACT_SILU) return z * recip(1.f + pow2(-1.442695041f * z));
   return z;
 }
 
-// The slope from the same forms (normcdff, tanhf and full divisions took the
-// dz pass to 3.3 times its HBM time). With E = exp(-v) and s = 1 / (1 + E),
-// 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0.
 template <int ACT>
 RNX_DEVICE float act_grad(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
   if (ACT == MOE_ACT_GELU) {                               // Phi(z) + z phi(z)
-    const float x = fabsf(z) * 0.7071067811865476f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    const float g = __expf(-x * x);
-    const float tail = 0.5f * poly * g;
-    return fmaf(z * 0.3989422804014327f, g, z > 0.f ? 1.f - tail : tail);
+    float g;
+    const float cdf = normal_cdf(z, g);
+    return fmaf(z * 0.3989422804014327f, g, cdf);
   }
   if (ACT == MOE_ACT_GELU_TANH) {
-    const float z2 = z * z;
-    const float E = __expf(-1.5957691216057308f * fmaf(0.044715f * z2, z, z));
-    const float s = __fdividef(1.f, 1.f + E);
-    return fmaf(z * s * fminf(E * s, 1.f), 1.5957691216057308f * fmaf(3.f * 0.044715f, z2, 1.f), s);
+    const float z2 = z * z, E = pow2(z * fmaf(-0.10294325f, z2, -2.3022082f)), s = recip(1.f + E);
+    return fmaf(z * s * fminf(E * s, 1.f), fmaf(0.21406445f, z2, 1.5957691f), s);
   }
   if (ACT == MOE_ACT_SILU) {
-    const float E = __expf(-z), s = __fdividef(1.f, 1.f + E);
+    const float E = pow2(-1.442695041f * z), s = recip(1.f + E);
     return fmaf(z * s, fminf(E * s, 1.f), s);
   }
   return 1.f;
@@ -400,8 +417,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] += __uint_as_float(res[i]);
     if (vec) {
-      if (ep.z) *reinterpret_cast<uint2*>(ep.z + row * ep.ldz + m) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      *reinterpret_cast<uint2*>(ep.out + row * ep.ldo + m) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      if (ep.z) *reinterpret_cast<uint2*>(ep.z + row * ep.ldz + m) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(ep.out + row * ep.ldo + m) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -751,10 +768,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<uint4*>(box_at(box, lane, j)) =
-                make_uint4(pack_bf16x2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
-                           pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
-                           pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
-                           pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
+                make_uint4(pack2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
+                           pack2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
+                           pack2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
+                           pack2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
           box_store(box, &q.tma_z, ep.z, ep.ldz, row0, col0, rows, cols, ep.vec, lane);
           box_free(lane);
         }
@@ -777,8 +794,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               y[2 * e] += f.x, y[2 * e + 1] += f.y;
             }
           }
-          *at = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                           pack_bf16x2(y[6], y[7]));
+          *at = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
+                           pack2(y[6], y[7]));
         }
         box_store(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
       }
@@ -874,8 +891,8 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long
       if (!dz) continue;
       uint16_t* pd = dz + r * lddz;
       if (whole) {
-        *reinterpret_cast<uint4*>(pd + c0) = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
-                                                        pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
+        *reinterpret_cast<uint4*>(pd + c0) = make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]),
+                                                        pack2(g[4], g[5]), pack2(g[6], g[7]));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)

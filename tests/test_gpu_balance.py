@@ -206,6 +206,29 @@ def test_extreme_logits():
     assert not torch.isnan(out[:5]).any() and torch.isnan(out[5]).all()
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last sequence's results and gradients."""
+    T, E, k, last = 7_500_000, 288, 2, 60
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.randn(T, E, device="cuda", generator=g)
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=g, dtype=torch.int32)
+    cfg, off = _cfg(E, k), torch.tensor([0, T - last, T], dtype=torch.int32, device="cuda")
+    counts, mean = torch.empty(2, E, dtype=torch.int32, device="cuda"), torch.empty(2, E, device="cuda")
+    loss, out = torch.empty(2, device="cuda"), torch.empty(T, E, device="cuda")
+    ws = capi.alloc_balance_workspace(cfg, T, 2)
+    capi.moe_balance_loss(cfg, logits, ids, 0.1, counts, mean, loss, ws, seq_offsets=off)
+    assert int(counts[0].sum()) == (T - last) * k
+    assert abs(float(mean[0].double().sum()) - 1) <= (T / 148 / 16 + 148 + 2 * E + 64) * U    # the sums' longest chain
+    d_loss, d_w = torch.ones(2, device="cuda"), torch.randn(T, k, device="cuda", generator=g) * 1e-3
+    capi.moe_router_backward(cfg, logits, ids, out, d_weights=d_w, coef=0.1, counts=counts, d_loss=d_loss, seq_offsets=off)
+    tail = slice(T - last, T)
+    cnt, m, l, grad, mag = _reference(logits[tail].cpu(), ids[tail].cpu(), [0, last], E, k, 0.1, None, d_loss[:1].cpu(),
+                                      d_w[tail].cpu())
+    assert torch.equal(counts[1:].cpu().long(), cnt)
+    assert ((mean[1:].cpu().double() - m).abs() <= (last + 2 * E + 64) * U * m).all()
+    assert ((out[tail].cpu().double() - grad).abs() <= (E + 64) * 2 * U * mag + 1e-40).all()
+
+
 def test_no_tokens_and_no_sequences():
     counts, mean, loss = _run(0, 16, 2, None, 1.0, torch.zeros(0, 16), torch.zeros(0, 2, dtype=torch.int32))
     assert not counts.any() and not mean.any() and not loss.any()

@@ -8,6 +8,9 @@ activation and its slope (bounded by 1.13) are evaluated in fp32 to a few
 steps: 2^-20 of |z| + 1. A result rounded to bf16 moves by at most 2^-8 of
 itself. dz enters its products rounded to bf16 (2^-8 of each element)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -295,6 +298,69 @@ def test_repeats_graphs_and_streams(T, K, N):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o[k], want[n][k]) for k in outs)
+
+
+def test_offsets_past_32_bits():
+    """Outputs and operands of more than 2^31 elements: the last rows and columns."""
+    T, K, N = 36000, 64, 60000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF16)  # noqa: E731
+    x, w, b = rn(T, K), rn(N, K) / 8, rn(N)
+    y, z = torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda")
+    ws = capi.alloc_linear_workspace(x, w)
+    capi.linear_bf16(x, w, y, ws, bias=b, act="silu", z=z)
+    for rows in (slice(0, 3), slice(T - 200, T)):
+        _check_forward(x[rows], w, b, None, y[rows], z[rows], "silu")
+    dy = y                                           # any values of its size
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device="cuda")
+    ws = capi.alloc_linear_backward_workspace(dy, x, w)
+    capi.linear_bf16_backward(dy, x, w, ws, z=z, act="silu", dx=dx, dw=dw, db=db)
+    capi.moe_read_device_status(ws)
+    rows, cols = slice(T - 100, T), slice(N - 100, N)
+    G, Z = dy[rows].to(F64), z[rows].to(F64)
+    dz, e = G * _slope("silu", Z), 2.0 ** -20 * G.abs() * (1 + Z.abs())
+    W = w.to(F64).abs()
+    tol = HALF * (dz @ w.to(F64)).abs() + 1.01 * ((HALF + _acc(N)) * (dz.abs() @ W) + e @ W)
+    assert ((dx[rows].to(F64) - dz @ w.to(F64)).abs() <= tol).all()
+    G, Z, X = dy[:, cols].to(F64), z[:, cols].to(F64), x.to(F64)
+    dz, e = G * _slope("silu", Z), 2.0 ** -20 * G.abs() * (1 + Z.abs())
+    tol = HALF * (dz.T @ X).abs() + 1.01 * ((HALF + _acc(T)) * (dz.abs().T @ X.abs()) + e.T @ X.abs())
+    assert ((dw[cols].to(F64) - dz.T @ X).abs() <= tol).all()
+    assert ((db[cols].to(F64) - dz.sum(0)).abs() <= 1.01 * ((T + 8) * 2.0 ** -24 * dz.abs().sum(0) + e.sum(0))).all()
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    code = """
+import torch
+from routed_nvfp4_expert_b200 import capi
+BF = torch.bfloat16
+x, w, b = torch.randn(300, 250).to(BF).cuda(), torch.randn(400, 250).to(BF).cuda(), torch.randn(400).to(BF).cuda()
+y, z, dx, dw = (torch.empty(*s, dtype=BF, device="cuda") for s in ((300, 400), (300, 400), (300, 250), (400, 250)))
+db = torch.empty(400, device="cuda")
+cfg = capi.SiteConfig(256, 128, 0, 500, 0, 500, 4, 2.5, 7.0)
+logits, ids = torch.randn(300, 500, device="cuda"), torch.randint(0, 500, (300, 4), device="cuda", dtype=torch.int32)
+counts, mean, loss = torch.empty(1, 500, dtype=torch.int32, device="cuda"), torch.empty(1, 500, device="cuda"), torch.empty(1, device="cuda")
+d_logits, one = torch.empty(300, 500, device="cuda"), torch.ones(1, device="cuda")
+ws, wsb, wsl = capi.alloc_linear_workspace(x, w), capi.alloc_linear_backward_workspace(y, x, w), capi.alloc_balance_workspace(cfg, 300)
+def calls():
+    capi.linear_bf16(x, w, y, ws, bias=b, act="gelu", z=z)
+    capi.linear_bf16_backward(y, x, w, wsb, z=z, act="gelu", dx=dx, dw=dw, db=db)
+    capi.moe_balance_loss(cfg, logits, ids, 0.1, counts, mean, loss, wsl)
+    capi.moe_router_backward(cfg, logits, ids, d_logits, coef=0.1, counts=counts, d_loss=one)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, z, dx, dw, db, counts, mean, loss, d_logits)]
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, t) for a, t in zip(got, (y, z, dx, dw, db, counts, mean, loss, d_logits)))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_two_calls_at_once_with_workspaces_of_their_own():
