@@ -360,13 +360,18 @@ def moe_unpermute_combine(cfg: SiteConfig, rows, T: int, plan: MoePlan, ids, sha
 # comparisons per tensor; what went wrong is worked out only when one fails.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _device_and_stream(stream):
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-    if stream is None and _raw_stream is not None and dev >= 0:
+def _device_and_stream(t, stream):
+    """The current device, where the call's first tensor t has to be (each of
+    them is compared with it), and the stream as an integer."""
+    if t.get_device() < 0:
+        return -2, None                      # no device matches: the tensor itself is refused
+    dev = torch.cuda.current_device()
+    if stream is None and _raw_stream is not None:
         return dev, _raw_stream(dev)
-    return dev, _stream(stream) if dev >= 0 else None
+    return dev, _stream(stream)
 
 
 def _refuse(t, name: str, dtype, shape):
@@ -417,8 +422,8 @@ def moe_balance_loss(cfg: SiteConfig, logits, ids, coef: float, counts, mean_sco
     fp32 [B, E], loss fp32 [B] (B sequences of seq_offsets int32 [B + 1], one
     when it is None)."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
-    f32, i32 = torch.float32, torch.int32
-    dev, st = _device_and_stream(stream)
+    f32, i32 = _F32, _I32
+    dev, st = _device_and_stream(logits, stream)
     _check(lib().moe_balance_loss(
         C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
         _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef, _arg(counts, "counts", i32, (B, E), dev),
@@ -431,8 +436,8 @@ def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, 
     """Gradient of the logits from the routing weights (d_weights fp32 [T, k])
     and the balance loss (counts of moe_balance_loss and d_loss fp32 [B])."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
-    f32, i32 = torch.float32, torch.int32
-    dev, st = _device_and_stream(stream)
+    f32, i32 = _F32, _I32
+    dev, st = _device_and_stream(logits, stream)
     _check(lib().moe_router_backward(
         C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
         _arg(d_weights, "d_weights", f32, (T, k), dev), _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef,
@@ -446,12 +451,12 @@ def _rows(t, name: str, shape, dev: int):
     """(pointer, row pitch) of a bf16 matrix whose rows are contiguous (None passes)."""
     if t is None:
         return None, 0
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
-        _refuse(t, name, torch.bfloat16, shape)
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, _BF16, shape)
     pitch, step = t.stride()
     rows, cols = shape
     if step != 1 and cols > 1:
-        _refuse(t, name, torch.bfloat16, shape)
+        _refuse(t, name, _BF16, shape)
     return t.data_ptr(), pitch if rows > 1 or pitch >= cols else cols
 
 
@@ -484,7 +489,7 @@ def linear_bf16(x, w, y, ws, bias=None, residual=None, act: str = "none", z=None
     """y = act(x w^T + bias) + residual; z receives the pre-activation. x [T, K],
     w [N, K], bias [N], residual, z, y [T, N], all bf16; rows may be strided."""
     (T, K), N = x.shape, w.shape[0]
-    dev, st = _device_and_stream(stream)
+    dev, st = _device_and_stream(x, stream)
     out = (T, N)
     xp, ldx = _rows(x, "x", (T, K), dev)
     wp, ldw = _rows(w, "w", (N, K), dev)
@@ -492,14 +497,14 @@ def linear_bf16(x, w, y, ws, bias=None, residual=None, act: str = "none", z=None
     zp, ldz = _rows(z, "z", out, dev)
     yp, ldy = _rows(y, "y", out, dev)
     _check(lib().linear_bf16(_activation(act), xp, ldx, T, K, wp, ldw, N,
-                             _arg(bias, "bias", torch.bfloat16, (N,), dev), rp, ldr, zp, ldz, yp, ldy, *_ws(ws, dev), st))
+                             _arg(bias, "bias", _BF16, (N,), dev), rp, ldr, zp, ldz, yp, ldy, *_ws(ws, dev), st))
 
 
 def linear_bf16_backward(dy, x, w, ws, z=None, act: str = "none", dx=None, dw=None, db=None, stream=None):
     """dz = dy act'(z); dx = dz w, dw = dz^T x (bf16), db = sum of dz over the
     tokens (fp32 [N]); each output may be None, not all."""
     (T, K), N = x.shape, w.shape[0]
-    dev, st = _device_and_stream(stream)
+    dev, st = _device_and_stream(x, stream)
     dyp, lddy = _rows(dy, "dy", (T, N), dev)
     zp, ldz = _rows(z, "z", (T, N), dev)
     xp, ldx = _rows(x, "x", (T, K), dev)
@@ -507,7 +512,7 @@ def linear_bf16_backward(dy, x, w, ws, z=None, act: str = "none", dx=None, dw=No
     dxp, lddx = _rows(dx, "dx", (T, K), dev)
     dwp, lddw = _rows(dw, "dw", (N, K), dev)
     _check(lib().linear_bf16_backward(_activation(act), dyp, lddy, zp, ldz, xp, ldx, T, K, wp, ldw, N, dxp, lddx, dwp,
-                                      lddw, _arg(db, "db", torch.float32, (N,), dev), *_ws(ws, dev), st))
+                                      lddw, _arg(db, "db", _F32, (N,), dev), *_ws(ws, dev), st))
 
 
 def moe_workspace_views(cfg: SiteConfig, T: int, path: int, ws) -> MoeViews:
