@@ -398,15 +398,16 @@ def _ws(ws, dev: int):
     """(pointer, bytes) of a workspace tensor."""
     if ws.get_device() != dev or not ws.is_contiguous():
         _refuse(ws, "ws", ws.dtype, tuple(ws.shape))
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _seqs(seq_offsets) -> int:
     if seq_offsets is None:
         return 1
-    if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
+    shape = seq_offsets.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise ValueError("seq_offsets: expected num_seqs + 1 offsets")
-    return seq_offsets.numel() - 1
+    return shape[0] - 1
 
 
 def alloc_balance_workspace(cfg: SiteConfig, T: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
@@ -422,12 +423,11 @@ def moe_balance_loss(cfg: SiteConfig, logits, ids, coef: float, counts, mean_sco
     fp32 [B, E], loss fp32 [B] (B sequences of seq_offsets int32 [B + 1], one
     when it is None)."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
-    f32, i32 = _F32, _I32
     dev, st = _device_and_stream(logits, stream)
     _check(lib().moe_balance_loss(
-        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
-        _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef, _arg(counts, "counts", i32, (B, E), dev),
-        _arg(mean_scores, "mean_scores", f32, (B, E), dev), _arg(loss, "loss", f32, (B,), dev),
+        C.byref(cfg.c()), _arg(logits, "logits", _F32, (T, E), dev), _arg(ids, "ids", _I32, (T, k), dev), T,
+        _arg(seq_offsets, "seq_offsets", _I32, (B + 1,), dev), B, coef, _arg(counts, "counts", _I32, (B, E), dev),
+        _arg(mean_scores, "mean_scores", _F32, (B, E), dev), _arg(loss, "loss", _F32, (B,), dev),
         *_ws(ws, dev), st))
 
 
@@ -436,13 +436,12 @@ def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, 
     """Gradient of the logits from the routing weights (d_weights fp32 [T, k])
     and the balance loss (counts of moe_balance_loss and d_loss fp32 [B])."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
-    f32, i32 = _F32, _I32
     dev, st = _device_and_stream(logits, stream)
     _check(lib().moe_router_backward(
-        C.byref(cfg.c()), _arg(logits, "logits", f32, (T, E), dev), _arg(ids, "ids", i32, (T, k), dev), T,
-        _arg(d_weights, "d_weights", f32, (T, k), dev), _arg(seq_offsets, "seq_offsets", i32, (B + 1,), dev), B, coef,
-        _arg(counts, "counts", i32, (B, E), dev), _arg(d_loss, "d_loss", f32, (B,), dev),
-        _arg(d_logits, "d_logits", f32, (T, E), dev), st))
+        C.byref(cfg.c()), _arg(logits, "logits", _F32, (T, E), dev), _arg(ids, "ids", _I32, (T, k), dev), T,
+        _arg(d_weights, "d_weights", _F32, (T, k), dev), _arg(seq_offsets, "seq_offsets", _I32, (B + 1,), dev), B, coef,
+        _arg(counts, "counts", _I32, (B, E), dev), _arg(d_loss, "d_loss", _F32, (B,), dev),
+        _arg(d_logits, "d_logits", _F32, (T, E), dev), st))
 
 
 # ------------------------------------------------------------------ BF16 linear layer

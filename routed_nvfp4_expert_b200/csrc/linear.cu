@@ -821,12 +821,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- row pitch
+// Rows whose pitch is not a multiple of 16 bytes cannot be a TMA operand; they
+// are copied to a pitch that is (columns behind the last are never read: the
+// tensor map ends at `cols`). Up to two operands in one launch: the forward's
+// first, or CTAs behind those of the backward's dz pass.
+struct PackJob {
+  const uint16_t* src;
+  uint16_t* dst;
+  long long ld_src, ld_dst;
+  int rows, cols;
+  unsigned items;      // 256-column pieces, set by launch_pack
+};
+struct PackParams {
+  PackJob job[2];
+  int n;
+  uint32_t* clear;     // status word (the pack is the call's first launch)
+};
+// A warp per 256 columns of a row (fewer than 2^31 of those fit the device);
+// CTAs of eight warps.
+RNX_DEVICE void pack_rows(const PackParams& p, unsigned cta, unsigned ctas) {
+  const int lane = threadIdx.x & 31;
+  const unsigned first = p.job[0].items, items = first + p.job[1].items;
+  for (unsigned at = cta * 8 + (threadIdx.x >> 5); at < items; at += ctas * 8) {
+    const PackJob& d = p.job[at >= first];
+    const unsigned i = at >= first ? at - first : at, chunks = (d.cols + 255) / 256, r = i / chunks;
+    const int c = 256 * (int)(i - r * chunks) + 8 * lane;
+    if (c >= d.cols) continue;
+    const uint16_t* s = d.src + r * d.ld_src + c;
+    uint32_t e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = c + k < d.cols ? s[k] : 0u;
+    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) =
+        make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+}
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
+  pack_rows(p, blockIdx.x, gridDim.x);
+}
+
 // ---------------------------------------------------------------- dz and db
 // dz = dy act'(z) in bf16 and the column sums of each chunk of rows in fp32
 // (rows of a warp in order, then the warps). A CTA owns 256 columns of one
 // chunk; a warp has four rows' loads in flight together. VEC: 16-byte loads,
 // eight consecutive columns per lane; otherwise columns lane + 32 i. HBM-bound:
-// 6 T N bytes (dy, z, dz).
+// 6 T N bytes (dy, z, dz). The CTAs behind `strips` x chunks copy operands.
 constexpr int kDzRows = 4;
 
 RNX_DEVICE void unpack8(const uint4& u, float* f) {
@@ -841,17 +883,24 @@ RNX_DEVICE void unpack8(const uint4& u, float* f) {
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long long lddy, const uint16_t* z,
                                                         long long ldz, int T, int N, int rows_per_cta, uint16_t* dz,
-                                                        long long lddz, float* db_part, uint32_t* clear) {
+                                                        long long lddz, float* db_part, uint32_t* clear,
+                                                        unsigned strips, unsigned ctas,
+                                                        const __grid_constant__ PackParams pk) {
   __shared__ float red[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * 256 + (VEC ? 8 * lane : lane);
+  const unsigned chunk = blockIdx.x / strips, strip = blockIdx.x - chunk * strips;
+  const int c0 = strip * 256 + (VEC ? 8 * lane : lane);
   constexpr int kStep = VEC ? 1 : 32;
-  const int r0 = blockIdx.y * rows_per_cta, r1 = min(T, r0 + rows_per_cta);
+  const int r0 = chunk * rows_per_cta, r1 = min(T, r0 + rows_per_cta);
   const bool whole = VEC && c0 + 8 <= N;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   pdl_wait();
   pdl_trigger();
-  if (clear && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) *clear = 0u;
+  if (clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0u;
+  if (blockIdx.x >= ctas) {
+    pack_rows(pk, blockIdx.x - ctas, gridDim.x - ctas);
+    return;
+  }
   for (int base = r0 + warp; base < r1; base += 8 * kDzRows) {
     uint4 u[kDzRows], uz[kDzRows];
 #pragma unroll
@@ -904,12 +953,12 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[warp][(VEC ? 8 * lane : lane) + kStep * i] = acc[i];
   __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  const int c = strip * 256 + threadIdx.x;
   if (c < N) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += red[w][threadIdx.x];
-    db_part[(size_t)blockIdx.y * N + c] = v;
+    db_part[(size_t)chunk * N + c] = v;
   }
 }
 
@@ -918,43 +967,6 @@ __global__ void __launch_bounds__(32) linear_db_kernel(const DbJoin d) {
   pdl_wait();
   pdl_trigger();
   join_db(d, blockIdx.x, gridDim.x, threadIdx.x);
-}
-
-// ---------------------------------------------------------------- row pitch
-// Rows whose pitch is not a multiple of 16 bytes cannot be a TMA operand; they
-// are copied to a pitch that is (columns behind the last are never read: the
-// tensor map ends at `cols`). Up to two operands in one launch.
-struct PackJob {
-  const uint16_t* src;
-  uint16_t* dst;
-  long long ld_src, ld_dst;
-  int rows, cols;
-  unsigned items;      // 256-column pieces, set by launch_pack
-};
-struct PackParams {
-  PackJob job[2];
-  int n;
-  uint32_t* clear;     // status word (the pack is the call's first launch)
-};
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
-  // a warp per 256 columns of a row (fewer than 2^31 of those fit the device)
-  const int lane = threadIdx.x & 31;
-  const unsigned first = p.job[0].items, items = first + p.job[1].items;
-  for (unsigned at = blockIdx.x * 8 + (threadIdx.x >> 5); at < items; at += gridDim.x * 8) {
-    const PackJob& d = p.job[at >= first];
-    const unsigned i = at >= first ? at - first : at, chunks = (d.cols + 255) / 256, r = i / chunks;
-    const int c = 256 * (int)(i - r * chunks) + 8 * lane;
-    if (c >= d.cols) continue;
-    const uint16_t* s = d.src + r * d.ld_src + c;
-    uint32_t e[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = c + k < d.cols ? s[k] : 0u;
-    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) =
-        make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -1232,26 +1244,33 @@ long long up8(long long v) { return (v + 7) / 8 * 8; }
 bool needs_copy(int rows, long long ld) { return rows > 1 && ld % 8; }
 long long operand_pitch(int rows, long long ld) { return rows > 1 ? ld : up8(ld); }
 
-cudaError_t launch_pack(PackParams p, cudaStream_t st) {
-  if (p.n == 0) return cudaSuccess;
+// Counts the jobs' items; CTAs for them in `grid`.
+bool plan_pack(PackParams& p, unsigned& grid) {
   long long items = 0;
   for (int i = 0; i < p.n; ++i) {
     const long long n = p.job[i].rows * ceil_div(p.job[i].cols, 256);
     p.job[i].items = (unsigned)n;
     items += n;
   }
-  if (items > 1ll << 31) return cudaErrorInvalidValue;
-  const int grid = (int)std::min<long long>((items + 7) / 8, 16 * kNumSMs);
+  grid = (unsigned)std::min<long long>((items + 7) / 8, 16 * kNumSMs);
+  return items <= 1ll << 31;
+}
+
+cudaError_t launch_pack(PackParams p, cudaStream_t st) {
+  if (p.n == 0) return cudaSuccess;
+  unsigned grid;
+  if (!plan_pack(p, grid)) return cudaErrorInvalidValue;
   return launch_pdl(pack_rows_kernel, dim3(grid), dim3(256), 0, st, p);
 }
 
 template <int ACT>
-cudaError_t launch_dz(bool vec, dim3 grid, cudaStream_t st, const uint16_t* dy, long long lddy, const uint16_t* z,
-                      long long ldz, int T, int N, int rows, uint16_t* dz, long long lddz, float* part, uint32_t* clear) {
-  if (vec) return launch_pdl(linear_dz_kernel<ACT, true>, grid, dim3(256), 0, st, dy, lddy, z, ldz, T, N, rows, dz, lddz, part,
-                             clear);
-  return launch_pdl(linear_dz_kernel<ACT, false>, grid, dim3(256), 0, st, dy, lddy, z, ldz, T, N, rows, dz, lddz, part,
-                    clear);
+cudaError_t launch_dz(bool vec, cudaStream_t st, const uint16_t* dy, long long lddy, const uint16_t* z, long long ldz,
+                      int T, int N, int rows, uint16_t* dz, long long lddz, float* part, uint32_t* clear, PackParams pk) {
+  unsigned more;
+  if (!plan_pack(pk, more)) return cudaErrorInvalidValue;
+  const unsigned strips = (unsigned)ceil_div(N, 256), ctas = strips * (unsigned)ceil_div(T, rows);
+  return launch_pdl(vec ? linear_dz_kernel<ACT, true> : linear_dz_kernel<ACT, false>, dim3(ctas + more), dim3(256), 0, st,
+                    dy, lddy, z, ldz, T, N, rows, dz, lddz, part, clear, strips, ctas, pk);
 }
 
 // Rows per CTA of the dz pass: one round of loads, more where that gives over
@@ -1331,9 +1350,7 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     ldw = up8(a.K);
     pk.job[pk.n++] = PackJob{a.w, reinterpret_cast<uint16_t*>(base + L.w), a.ldw, ldw, a.N, a.K};
   }
-  pk.clear = status;
-  if ((e = launch_pack(pk, st)) != cudaSuccess) return e;
-  bool clear = pk.n == 0;              // for the call's first launch
+  bool clear = true;                   // for the call's first launch
 
   // dz: dy itself where the layer has no activation and dy can be an operand
   const bool products = a.dx || a.dw, write_dz = products && (act != MOE_ACT_NONE || needs_copy(a.T, a.lddy));
@@ -1345,10 +1362,9 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     const long long pitch = up8(a.N);
     const int rows = dz_rows(a.T, a.N), chunks = (a.T + rows - 1) / rows;
     float* part = a.db ? reinterpret_cast<float*>(base + L.part) : nullptr;
-    const dim3 grid((a.N + 255) / 256, chunks);
     const bool vec = a.lddy % 8 == 0 && (act == MOE_ACT_NONE || a.ldz % 8 == 0);
     switch (act) {
-#define RNX_DZ(A) case A: e = launch_dz<A>(vec, grid, st, a.dy, a.lddy, a.z, a.ldz, a.T, a.N, rows, dst, pitch, part, clear ? status : nullptr); break
+#define RNX_DZ(A) case A: e = launch_dz<A>(vec, st, a.dy, a.lddy, a.z, a.ldz, a.T, a.N, rows, dst, pitch, part, status, pk); break
       RNX_DZ(MOE_ACT_NONE);
       RNX_DZ(MOE_ACT_RELU);
       RNX_DZ(MOE_ACT_GELU);
@@ -1364,6 +1380,10 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
       lddz = pitch;
     }
     if (a.db) db = DbJoin{part, a.db, chunks, a.N};
+  } else if (pk.n) {
+    pk.clear = status;
+    if ((e = launch_pack(pk, st)) != cudaSuccess) return e;
+    clear = false;
   }
   Product prod[2];
   int n = 0;
