@@ -140,6 +140,55 @@ RNX_DEVICE void ring_drain(uint64_t* full_bar, Ring at, int issued, int stages, 
   }
 }
 
+// ---------------------------------------------------------------- unaligned rows
+// Eight elements at p, of which `valid` belong to the row, by 16-byte loads.
+// ANY: p on any element; the one or two aligned pieces that hold the elements
+// are loaded here and shifted together in finish8. No piece is read that runs
+// past `end`, the matrix's end: there load8 returns false and finish8 takes the
+// elements one by one, as load8 without ANY does at a row's ragged end.
+struct Load8 {
+  uint4 lo, hi;
+};
+RNX_DEVICE uint4 load8_elements(const uint16_t* p, int valid) {
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = i < valid ? p[i] : 0u;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+template <bool ANY>
+RNX_DEVICE bool load8(Load8& v, const uint16_t* p, int valid, const uint16_t* end) {
+  if (!ANY) {
+    if (valid >= 8) v.lo = *reinterpret_cast<const uint4*>(p);
+    else v.lo = load8_elements(p, valid);
+    return true;
+  }
+  if (valid <= 0) return false;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+  const bool two = (reinterpret_cast<uintptr_t>(p) & 15) + 2 * min(valid, 8) > 16;
+  if (at + (two ? 32 : 16) > reinterpret_cast<uintptr_t>(end)) return false;
+  v.lo = *reinterpret_cast<const uint4*>(at);
+  v.hi = two ? *reinterpret_cast<const uint4*>(at + 16) : make_uint4(0u, 0u, 0u, 0u);
+  return true;
+}
+// 16 of the 32 bytes lo, hi, from byte `shift` (even, below 16).
+RNX_DEVICE uint4 shift16(const uint4& lo, const uint4& hi, uint32_t shift) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t a[6], b[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) a[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) b[i] = shift & 4 ? a[i + 1] : a[i];
+  const uint32_t bits = 8 * (shift & 2);
+  return make_uint4(__funnelshift_r(b[0], b[1], bits), __funnelshift_r(b[1], b[2], bits),
+                    __funnelshift_r(b[2], b[3], bits), __funnelshift_r(b[3], b[4], bits));
+}
+template <bool ANY>
+RNX_DEVICE uint4 finish8(const Load8& v, const uint16_t* p, int valid, bool loaded) {
+  if (!ANY) return v.lo;
+  if (!loaded) return load8_elements(p, valid);
+  return shift16(v.lo, v.hi, (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15));
+}
+
 struct Epilogue {
   const uint16_t* bias;       // per output feature, nullable
   const uint16_t* residual;   // nullable
@@ -446,8 +495,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // Warps: 0 and 3 = TMA producers of A and of B, 1 = MMA issuer (even CTA), 2 =
 // TMEM allocator, then db join, 4-11 = epilogue (lane quadrant w % 4, half of the columns each):
 // 64 columns at a time go through a swizzled 32-row box in shared memory, from
-// which one tensor store writes them (2-byte stores where the pitch or N is no
-// multiple of 8 elements).
+// which one tensor store writes them (the lanes' own stores where the pitch or N
+// is no multiple of 8 elements).
 // Every wait is bounded. No TMA load uses cluster multicast.
 
 constexpr int kPairM = 256;
@@ -527,7 +576,8 @@ RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
 
 // The box to global memory at column col0, row row0 (whole warp): one tensor
 // store, which ends at the tensor's edges by itself, or rows x cols elements
-// where the pitch rules a tensor map out. Before the box is written again:
+// where the pitch rules a tensor map out (4096 x 4096 x 4095, GELU with z and
+// residual: 269 us element by element). Before the box is written again:
 // box_free().
 RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, long long ld, int row0, int col0, int rows,
                           int cols, int vec, int lane) {
@@ -540,10 +590,21 @@ RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, l
     }
   } else {
     __syncwarp();
-    for (int r = 0; r < rows; ++r) {
+    // eight lanes per row: the aligned 16-byte pieces inside it, then the
+    // elements before the first (up to 7) and behind the last
+    const int l = lane & 7;
+#pragma unroll 1
+    for (int r = lane >> 3; r < rows; r += 4) {
       uint16_t* p = out + (row0 + r) * ld + col0;
-      if (lane < cols) p[lane] = *box_elem(box, r, lane);
-      if (lane + 32 < cols) p[lane + 32] = *box_elem(box, r, lane + 32);
+      const int head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2, from = head + 8 * l;
+      const int tail = cols < head ? cols : head + ((cols - head) & ~7);
+      if (from + 8 <= cols) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(box_at(box, r, l));
+        const uint4 hi = *reinterpret_cast<const uint4*>(box_at(box, r, (l + 1) & 7));
+        *reinterpret_cast<uint4*>(p + from) = shift16(lo, hi, 2 * head);
+      }
+      if (l < head && l < cols) p[l] = *box_elem(box, r, l);
+      if (tail + l < cols) p[tail + l] = *box_elem(box, r, tail + l);
     }
   }
 }
@@ -571,11 +632,26 @@ RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
   for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(box_at(box, 4 * i + (lane >> 3), lane & 7)) = b.v[i];
   __syncwarp();
 }
-RNX_DEVICE void box_load_scalar(uint8_t* box, const uint16_t* src, long long ld, int rows, int cols, int lane) {
-  for (int r = 0; r < rows; ++r) {
-    const uint16_t* p = src + r * ld;
-    if (lane < cols) *box_elem(box, r, lane) = p[lane];
-    if (lane + 32 < cols) *box_elem(box, r, lane + 32) = p[lane + 32];
+// The same from rows on any element, straight into the box. `end`: the matrix's.
+constexpr int kBoxRows = 4;
+RNX_DEVICE void box_load_any(uint8_t* box, const uint16_t* src, long long ld, int rows, int cols, const uint16_t* end,
+                             int lane) {
+  const int c = lane & 7;
+#pragma unroll 1
+  for (int r0 = lane >> 3; r0 < 32; r0 += 4 * kBoxRows) {
+    Load8 v[kBoxRows];
+    bool loaded[kBoxRows];
+#pragma unroll
+    for (int i = 0; i < kBoxRows; ++i) {
+      const int r = r0 + 4 * i;
+      loaded[i] = load8<true>(v[i], src + r * ld + 8 * c, r < rows ? cols - 8 * c : 0, end);
+    }
+#pragma unroll
+    for (int i = 0; i < kBoxRows; ++i) {
+      const int r = r0 + 4 * i;
+      *reinterpret_cast<uint4*>(box_at(box, r, c)) =
+          finish8<true>(v[i], src + r * ld + 8 * c, r < rows ? cols - 8 * c : 0, loaded[i]);
+    }
   }
   __syncwarp();
 }
@@ -777,7 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         if (res_src) {
           if (ep.vec) box_land(res, box, lane);
-          else box_load_scalar(box, res_src, ep.ldr, rows, cols, lane);
+          else box_load_any(box, res_src, ep.ldr, rows, cols, ep.residual + (q.M - 1) * ep.ldr + q.N, lane);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -838,25 +914,37 @@ struct PackParams {
   int n;
   uint32_t* clear;     // status word (the pack is the call's first launch)
 };
-// A warp per 256 columns of a row (fewer than 2^31 of those fit the device);
-// CTAs of eight warps.
+// A warp per 256 columns of a row (fewer than 2^31 of those fit the device),
+// two such pieces in flight; CTAs of eight warps.
+constexpr int kPackItems = 2;
 RNX_DEVICE void pack_rows(const PackParams& p, unsigned cta, unsigned ctas) {
   const int lane = threadIdx.x & 31;
-  const unsigned first = p.job[0].items, items = first + p.job[1].items;
-  for (unsigned at = cta * 8 + (threadIdx.x >> 5); at < items; at += ctas * 8) {
-    const PackJob& d = p.job[at >= first];
-    const unsigned i = at >= first ? at - first : at, chunks = (d.cols + 255) / 256, r = i / chunks;
-    const int c = 256 * (int)(i - r * chunks) + 8 * lane;
-    if (c >= d.cols) continue;
-    const uint16_t* s = d.src + r * d.ld_src + c;
-    uint32_t e[8];
+  const unsigned first = p.job[0].items, items = first + p.job[1].items, step = ctas * 8;
+  for (unsigned at = cta * 8 + (threadIdx.x >> 5); at < items; at += kPackItems * step) {
+    Load8 v[kPackItems];
+    const uint16_t* s[kPackItems];
+    uint16_t* d[kPackItems];
+    int valid[kPackItems];
+    bool loaded[kPackItems];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = c + k < d.cols ? s[k] : 0u;
-    *reinterpret_cast<uint4*>(d.dst + r * d.ld_dst + c) =
-        make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    for (int k = 0; k < kPackItems; ++k) {
+      const unsigned it = at + k * step;
+      valid[k] = 0;
+      if (it >= items) continue;
+      const PackJob& j = p.job[it >= first];
+      const unsigned i = it >= first ? it - first : it, chunks = (j.cols + 255) / 256, r = i / chunks;
+      const int c = 256 * (int)(i - r * chunks) + 8 * lane;
+      s[k] = j.src + r * j.ld_src + c;
+      d[k] = j.dst + r * j.ld_dst + c;
+      valid[k] = j.cols - c;
+      loaded[k] = load8<true>(v[k], s[k], valid[k], j.src + (j.rows - 1) * j.ld_src + j.cols);
+    }
+#pragma unroll
+    for (int k = 0; k < kPackItems; ++k)
+      if (valid[k] > 0) *reinterpret_cast<uint4*>(d[k]) = finish8<true>(v[k], s[k], valid[k], loaded[k]);
   }
 }
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
+__global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ PackParams p) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0u;
@@ -866,8 +954,8 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackParams p) {
 // ---------------------------------------------------------------- dz and db
 // dz = dy act'(z) in bf16 and the column sums of each chunk of rows in fp32
 // (rows of a warp in order, then the warps). A CTA owns 256 columns of one
-// chunk; a warp has four rows' loads in flight together. VEC: 16-byte loads,
-// eight consecutive columns per lane; otherwise columns lane + 32 i. HBM-bound:
+// chunk, eight consecutive ones per lane; a warp has four rows' loads in flight
+// together (ANY, rows off 16 bytes: two rows of twice the loads). HBM-bound:
 // 6 T N bytes (dy, z, dz). The CTAs behind `strips` x chunks copy operands.
 constexpr int kDzRows = 4;
 
@@ -880,19 +968,19 @@ RNX_DEVICE void unpack8(const uint4& u, float* f) {
   }
 }
 
-template <int ACT, bool VEC>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long long lddy, const uint16_t* z,
+template <int ACT, bool ANY>
+__global__ void __launch_bounds__(256, ANY ? 3 : 4) linear_dz_kernel(const uint16_t* dy, long long lddy, const uint16_t* z,
                                                         long long ldz, int T, int N, int rows_per_cta, uint16_t* dz,
                                                         long long lddz, float* db_part, uint32_t* clear,
                                                         unsigned strips, unsigned ctas,
                                                         const __grid_constant__ PackParams pk) {
+  constexpr int kRows = ANY ? kDzRows / 2 : kDzRows;
   __shared__ float red[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned chunk = blockIdx.x / strips, strip = blockIdx.x - chunk * strips;
-  const int c0 = strip * 256 + (VEC ? 8 * lane : lane);
-  constexpr int kStep = VEC ? 1 : 32;
+  const int c0 = strip * 256 + 8 * lane, valid = N - c0;
   const int r0 = chunk * rows_per_cta, r1 = min(T, r0 + rows_per_cta);
-  const bool whole = VEC && c0 + 8 <= N;
+  const uint16_t *dy_end = dy + (T - 1) * lddy + N, *z_end = z + (T - 1) * ldz + N;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   pdl_wait();
   pdl_trigger();
@@ -901,57 +989,37 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const uint16_t* dy, long
     pack_rows(pk, blockIdx.x - ctas, gridDim.x - ctas);
     return;
   }
-  for (int base = r0 + warp; base < r1; base += 8 * kDzRows) {
-    uint4 u[kDzRows], uz[kDzRows];
+  for (int base = r0 + warp; valid > 0 && base < r1; base += 8 * kRows) {
+    Load8 u[kRows], uz[kRows];
+    bool got[kRows], got_z[kRows];
 #pragma unroll
-    for (int k = 0; k < kDzRows; ++k) {
+    for (int k = 0; k < kRows; ++k) {
       const int r = base + 8 * k;
-      u[k] = uz[k] = make_uint4(0u, 0u, 0u, 0u);
       if (r >= r1) continue;
-      const uint16_t* py = dy + r * lddy;
-      const uint16_t* pz = z + r * ldz;
-      if (whole) {
-        u[k] = *reinterpret_cast<const uint4*>(py + c0);
-        if (ACT != MOE_ACT_NONE) uz[k] = *reinterpret_cast<const uint4*>(pz + c0);
-      } else {
-        uint32_t a[8], b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0 + kStep * i;
-          a[i] = c < N ? py[c] : 0u;
-          b[i] = ACT != MOE_ACT_NONE && c < N ? pz[c] : 0u;
-        }
-        u[k] = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
-        uz[k] = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
-      }
+      got[k] = load8<ANY>(u[k], dy + r * lddy + c0, valid, dy_end);
+      if (ACT != MOE_ACT_NONE) got_z[k] = load8<ANY>(uz[k], z + r * ldz + c0, valid, z_end);
     }
 #pragma unroll
-    for (int k = 0; k < kDzRows; ++k) {
+    for (int k = 0; k < kRows; ++k) {
       const int r = base + 8 * k;
       if (r >= r1) break;
       float g[8], a[8];
-      unpack8(u[k], g);
-      if (ACT != MOE_ACT_NONE) unpack8(uz[k], a);
+      unpack8(finish8<ANY>(u[k], dy + r * lddy + c0, valid, got[k]), g);
+      if (ACT != MOE_ACT_NONE) unpack8(finish8<ANY>(uz[k], z + r * ldz + c0, valid, got_z[k]), a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (ACT != MOE_ACT_NONE) g[i] *= act_grad<ACT>(a[i]);
         acc[i] += g[i];
       }
-      if (!dz) continue;
-      uint16_t* pd = dz + r * lddz;
-      if (whole) {
-        *reinterpret_cast<uint4*>(pd + c0) = make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]),
-                                                        pack2(g[4], g[5]), pack2(g[6], g[7]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c0 + kStep * i < N) pd[c0 + kStep * i] = f32_to_bf16_bits(g[i]);
-      }
+      // whole pieces: dz's rows are padded to them, and the padding is never read
+      if (dz)
+        *reinterpret_cast<uint4*>(dz + r * lddz + c0) = make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]),
+                                                                   pack2(g[4], g[5]), pack2(g[6], g[7]));
     }
   }
   if (!db_part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[warp][(VEC ? 8 * lane : lane) + kStep * i] = acc[i];
+  for (int i = 0; i < 8; ++i) red[warp][8 * lane + i] = acc[i];
   __syncthreads();
   const int c = strip * 256 + threadIdx.x;
   if (c < N) {
@@ -1240,6 +1308,9 @@ bool vec_ok(const Epilogue& e) {
 
 long long up8(long long v) { return (v + 7) / 8 * 8; }
 
+// Row pitch of a copied operand and of dz: whole 128-byte lines.
+long long copy_pitch(long long cols) { return (cols + 63) / 64 * 64; }
+
 // A single row's pitch is of no account.
 bool needs_copy(int rows, long long ld) { return rows > 1 && ld % 8; }
 long long operand_pitch(int rows, long long ld) { return rows > 1 ? ld : up8(ld); }
@@ -1264,12 +1335,12 @@ cudaError_t launch_pack(PackParams p, cudaStream_t st) {
 }
 
 template <int ACT>
-cudaError_t launch_dz(bool vec, cudaStream_t st, const uint16_t* dy, long long lddy, const uint16_t* z, long long ldz,
+cudaError_t launch_dz(bool any, cudaStream_t st, const uint16_t* dy, long long lddy, const uint16_t* z, long long ldz,
                       int T, int N, int rows, uint16_t* dz, long long lddz, float* part, uint32_t* clear, PackParams pk) {
   unsigned more;
   if (!plan_pack(pk, more)) return cudaErrorInvalidValue;
   const unsigned strips = (unsigned)ceil_div(N, 256), ctas = strips * (unsigned)ceil_div(T, rows);
-  return launch_pdl(vec ? linear_dz_kernel<ACT, true> : linear_dz_kernel<ACT, false>, dim3(ctas + more), dim3(256), 0, st,
+  return launch_pdl(any ? linear_dz_kernel<ACT, true> : linear_dz_kernel<ACT, false>, dim3(ctas + more), dim3(256), 0, st,
                     dy, lddy, z, ldz, T, N, rows, dz, lddz, part, clear, strips, ctas, pk);
 }
 
@@ -1289,9 +1360,9 @@ LinearLayout linear_layout(int T, int K, int N, long long ldx, long long ldw) {
   LinearLayout L{};
   size_t o = 256;                                             // status word
   L.x = o;
-  if (needs_copy(T, ldx)) o = up256(o + 2 * (size_t)T * up8(K));
+  if (needs_copy(T, ldx)) o = up256(o + 2 * (size_t)T * copy_pitch(K));
   L.w = o;
-  if (needs_copy(N, ldw)) o = up256(o + 2 * (size_t)N * up8(K));
+  if (needs_copy(N, ldw)) o = up256(o + 2 * (size_t)N * copy_pitch(K));
   L.dz = L.part = L.bytes = o;
   return L;
 }
@@ -1300,7 +1371,7 @@ LinearLayout linear_backward_layout(int T, int K, int N, long long ldx, long lon
   LinearLayout L = linear_layout(T, K, N, ldx, ldw);
   size_t o = L.bytes;
   L.dz = o;
-  o = up256(o + 2 * (size_t)T * up8(N));
+  o = up256(o + 2 * (size_t)T * copy_pitch(N));
   L.part = o;
   if (T > 0) o = up256(o + 4 * (size_t)N * ((T + dz_rows(T, N) - 1) / dz_rows(T, N)));
   L.bytes = o;
@@ -1313,21 +1384,23 @@ cudaError_t launch_linear(int act, const LinearArgs& a, void* ws, cudaStream_t s
   Operand x{a.x, operand_pitch(a.T, a.ldx), a.T, false}, w{a.w, operand_pitch(a.N, a.ldw), a.N, false};
   PackParams pk{};
   if (needs_copy(a.T, a.ldx)) {
-    x = Operand{reinterpret_cast<uint16_t*>(base + L.x), up8(a.K), a.T, false};
+    x = Operand{reinterpret_cast<uint16_t*>(base + L.x), copy_pitch(a.K), a.T, false};
     pk.job[pk.n++] = PackJob{a.x, reinterpret_cast<uint16_t*>(base + L.x), a.ldx, x.ld, a.T, a.K};
   }
   if (needs_copy(a.N, a.ldw)) {
-    w = Operand{reinterpret_cast<uint16_t*>(base + L.w), up8(a.K), a.N, false};
+    w = Operand{reinterpret_cast<uint16_t*>(base + L.w), copy_pitch(a.K), a.N, false};
     pk.job[pk.n++] = PackJob{a.w, reinterpret_cast<uint16_t*>(base + L.w), a.ldw, w.ld, a.N, a.K};
   }
-  pk.clear = reinterpret_cast<uint32_t*>(base);
-  cudaError_t e = launch_pack(pk, st);
-  if (e != cudaSuccess) return e;
   Epilogue ep{a.bias, a.residual, a.z, a.y, a.ldr, a.ldz, a.ldy, 0};
   ep.vec = vec_ok(ep);
   const Product prod{x, w, a.K, ep};
   uint32_t* status = reinterpret_cast<uint32_t*>(base);
   const Choice c = choose(&prod, 1);
+  if (pk.n) {
+    pk.clear = status;
+    const cudaError_t e = launch_pack(pk, st);
+    if (e != cudaSuccess) return e;
+  }
   if (c.width) return launch_pair(act, &prod, 1, c.width, DbJoin{}, status, pk.n == 0, st);
   return launch_split(act, &prod, 1, c.split, DbJoin{}, status, pk.n == 0, st);
 }
@@ -1342,12 +1415,12 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
   long long ldx = operand_pitch(a.T, a.ldx), ldw = operand_pitch(a.N, a.ldw);
   if (a.dw && needs_copy(a.T, a.ldx)) {
     x = reinterpret_cast<uint16_t*>(base + L.x);
-    ldx = up8(a.K);
+    ldx = copy_pitch(a.K);
     pk.job[pk.n++] = PackJob{a.x, reinterpret_cast<uint16_t*>(base + L.x), a.ldx, ldx, a.T, a.K};
   }
   if (a.dx && needs_copy(a.N, a.ldw)) {
     w = reinterpret_cast<uint16_t*>(base + L.w);
-    ldw = up8(a.K);
+    ldw = copy_pitch(a.K);
     pk.job[pk.n++] = PackJob{a.w, reinterpret_cast<uint16_t*>(base + L.w), a.ldw, ldw, a.N, a.K};
   }
   bool clear = true;                   // for the call's first launch
@@ -1359,12 +1432,12 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
   DbJoin db{};
   if (write_dz || a.db) {
     uint16_t* dst = write_dz ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
-    const long long pitch = up8(a.N);
+    const long long pitch = copy_pitch(a.N);
     const int rows = dz_rows(a.T, a.N), chunks = (a.T + rows - 1) / rows;
     float* part = a.db ? reinterpret_cast<float*>(base + L.part) : nullptr;
-    const bool vec = a.lddy % 8 == 0 && (act == MOE_ACT_NONE || a.ldz % 8 == 0);
+    const bool any = a.lddy % 8 || (act != MOE_ACT_NONE && a.ldz % 8);
     switch (act) {
-#define RNX_DZ(A) case A: e = launch_dz<A>(vec, st, a.dy, a.lddy, a.z, a.ldz, a.T, a.N, rows, dst, pitch, part, status, pk); break
+#define RNX_DZ(A) case A: e = launch_dz<A>(any, st, a.dy, a.lddy, a.z, a.ldz, a.T, a.N, rows, dst, pitch, part, status, pk); break
       RNX_DZ(MOE_ACT_NONE);
       RNX_DZ(MOE_ACT_RELU);
       RNX_DZ(MOE_ACT_GELU);
