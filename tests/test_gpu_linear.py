@@ -220,6 +220,37 @@ def test_backward_matches_the_formula(T, K, N, act, want, pitches):
     _check_backward(T, K, N, act, x, w, z, g, want, pitches)
 
 
+def _poisoned(t, pitch):
+    """The same rows at this pitch, NaN between them; the buffer ends with the last row's last element."""
+    rows, cols = t.shape
+    buf = torch.full(((rows - 1) * pitch + cols,), float("nan"), dtype=BF16, device="cuda")
+    v = torch.as_strided(buf, (rows, cols), (pitch, 1))
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("extra", range(8))
+@pytest.mark.parametrize("T,K,N", [(45, 203, 331), (1400, 264, 1090)])
+def test_rows_on_every_element_boundary(T, K, N, extra):
+    """Pitches of every residue mod 8, which put rows on every 2-byte offset of
+    a 16-byte piece, through the copies, the dz pass and the epilogues of both
+    kernels; nothing between the rows enters a result or is written."""
+    g = torch.Generator().manual_seed(T + extra)
+    x = _poisoned(_rand(g, T, K), K + extra)
+    w = _poisoned(_rand(g, N, K, scale=K ** -0.5), K + (extra + 3) % 8)
+    b = torch.randn(N, generator=g).to(BF16).cuda()
+    r = _poisoned(_rand(g, T, N), N + (extra + 5) % 8)
+    y, zo = _rand(g, T, N, pitch=N + 1 + extra), _rand(g, T, N, pitch=N + 1 + (extra + 2) % 8)
+    ws = capi.alloc_linear_workspace(x, w)
+    ws.fill_(0xFF)
+    capi.linear_bf16(x, w, y, ws, bias=b, residual=r, act="gelu", z=zo)
+    capi.moe_read_device_status(ws)
+    _check_forward(x, w, b, r, y, zo, "gelu")
+    assert _tail_untouched(y, T, N) and _tail_untouched(zo, T, N)
+    z = _poisoned(_rand(g, T, N), N + (extra + 1) % 8)
+    _check_backward(T, K, N, "silu", x, w, z, g, pitches=(1 + extra, 1 + (extra + 2) % 8, 1 + (extra + 5) % 8))
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_gradients_match_differences(act):
     """Directional differences of sum(dy * y) in 64 bits, through the forward's own kept z."""
