@@ -615,7 +615,7 @@ int balance_blocks(int T) {
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
                                 cudaStream_t st) {
-  const int blocks = balance_blocks(T);
+  const int blocks = T <= kBalanceManyMaxT && T <= kBalanceManyMean * (long long)B ? 0 : balance_blocks(T);
   float* psum = static_cast<float*>(scratch);
   BalanceParams p{logits, ids, off, T, E, k, B, balance_rows_per_block(T), coef, psum,
                   reinterpret_cast<int*>(psum + (size_t)(blocks + B) * E), counts, mean, loss};

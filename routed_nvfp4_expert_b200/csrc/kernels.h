@@ -314,8 +314,14 @@ cudaError_t launch_w4a16_grouped_gemm(const W4a16GemmArgs& a, cudaStream_t st);
 // launch, 6.9 us at 128 x 288); longer ones by one CTA per SM and a join (7.9
 // against 10.1 us at 256).
 constexpr int kBalanceSeqMaxT = 128;
+// Many short sequences are too: the second form pays 1 to 3 us for every
+// sequence that ends inside a CTA's rows (62 sequences of 512 x 288 in all: 4.2
+// against 15.8 us; of 2048 x 288: 8.2 against 13.3 us). The host does not see
+// the lengths; were one sequence to hold all 2048 rows, it would take 47 us.
+constexpr int kBalanceManyMaxT = 2048, kBalanceManyMean = 64;
 // CTAs of the first step of launch_balance_loss (0: the one-launch form); its
-// scratch holds (blocks + B) * E floats and as many ints.
+// scratch holds (blocks + B) * E floats and as many ints (also where many short
+// sequences leave it unused, so that fewer sequences never need more).
 int balance_blocks(int T);
 // off: [B + 1] ascending row offsets (NULL with B = 1: all T rows).
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,

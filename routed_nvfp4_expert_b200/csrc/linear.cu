@@ -49,6 +49,8 @@ RNX_DEVICE float recip(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+RNX_DEVICE void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Two values rounded to bf16 in one instruction (lo in the low half).
 RNX_DEVICE uint32_t pack2(float lo, float hi) {
   uint32_t w;
@@ -198,25 +200,33 @@ struct Epilogue {
   int vec;                    // rows of residual, z and out all start on 16-byte boundaries
 };
 
-// db from the column sums of the row chunks, by one warp per CTA: four lanes
-// per column take every fourth chunk in order, then add theirs.
+// db from the column sums of the row chunks, by `units` warps: four lanes per
+// column take every fourth chunk in order, then add theirs; a warp has four
+// columns per lane group at work (eight columns in all left 7872 columns to 20
+// rounds of memory latency in a launch of few CTAs: 10 us).
 struct DbJoin {
   const float* part;          // [chunks, n]
   float* db;                  // nullable
   int chunks, n;
 };
-RNX_DEVICE void join_db(const DbJoin& d, int cta, int ctas, int lane) {
+RNX_DEVICE void join_db(const DbJoin& d, int unit, int units, int lane) {
   if (!d.db) return;
-  for (int c0 = cta * 8; c0 < d.n; c0 += ctas * 8) {        // warp-uniform
+  for (int c0 = unit * 32; c0 < d.n; c0 += units * 32) {    // warp-uniform
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     const int c = c0 + lane / 4;
-    float v = 0.f;
-    if (c < d.n) {
-#pragma unroll 8
-      for (int i = lane % 4; i < d.chunks; i += 4) v += d.part[(size_t)i * d.n + c];
+#pragma unroll 4
+    for (int i = lane % 4; i < d.chunks; i += 4) {
+      const float* src = d.part + (size_t)i * d.n + c;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (c + 8 * s < d.n) v[s] += src[8 * s];
     }
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    v += __shfl_xor_sync(0xffffffffu, v, 2);
-    if (c < d.n && lane % 4 == 0) d.db[c] = v;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      v[s] += __shfl_xor_sync(0xffffffffu, v[s], 1);
+      v[s] += __shfl_xor_sync(0xffffffffu, v[s], 2);
+      if (c + 8 * s < d.n && lane % 4 == 0) d.db[c + 8 * s] = v[s];
+    }
   }
 }
 
@@ -235,7 +245,7 @@ RNX_DEVICE void join_db(const DbJoin& d, int cta, int ctas, int lane) {
 // read.) Up to two products share a
 // launch (dx and dW of few tokens); a reduction of fewer steps than S leaves
 // the last ranks without a part of their own.
-// Warps: 0 = TMA producer, 1 = MMA issuer, 2 = TMEM allocator, 3 = db join,
+// Warps: 0 = TMA producer, 1 = MMA issuer, 2 = TMEM allocator, 3-7 = db join,
 // 4-7 = TMEM readers; all eight reduce and store. Every wait is bounded; a
 // timeout sets the status word, and the CTA still meets its cluster's barrier.
 
@@ -369,8 +379,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     if (elect_one()) mma_commit(&mma_done);
     __syncwarp();
     if (!mbar_wait_poll(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
-  } else if (warp == 3) {
-    join_db(p.db, (int)blockIdx.x, (int)gridDim.x, lane);
+  } else if (warp >= 3) {
+    join_db(p.db, (int)blockIdx.x * 5 + warp - 3, (int)gridDim.x * 5, lane);
   }
 
   // the producer and the issuer are through: every copy has landed and every
@@ -574,10 +584,30 @@ RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
   return reinterpret_cast<uint16_t*>(box_at(box, row, col >> 3)) + (col & 7);
 }
 
+// A box to rows that no tensor map describes: eight lanes per row, the aligned
+// 16-byte pieces inside it, then the elements before the first (up to 7) and
+// behind the last. (4096 x 640 -> 4691 with residual: 215 us by elements, 64 us
+// by pieces; words of two columns, for even pitches, gain 5% without a residual
+// and lose 11% with one.)
+RNX_DEVICE void box_store_pieces(uint8_t* box, uint16_t* out, long long ld, int rows, int cols, int lane) {
+  const int l = lane & 7;
+#pragma unroll 1
+  for (int r = lane >> 3; r < rows; r += 4) {
+    uint16_t* p = out + r * ld;
+    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2, from = head + 8 * l;
+    const int tail = cols < head ? cols : head + ((cols - head) & ~7);
+    if (from + 8 <= cols) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(box_at(box, r, l));
+      const uint4 hi = *reinterpret_cast<const uint4*>(box_at(box, r, (l + 1) & 7));
+      *reinterpret_cast<uint4*>(p + from) = shift16(lo, hi, 2 * head);
+    }
+    if (l < head && l < cols) p[l] = *box_elem(box, r, l);
+    if (tail + l < cols) p[tail + l] = *box_elem(box, r, tail + l);
+  }
+}
 // The box to global memory at column col0, row row0 (whole warp): one tensor
 // store, which ends at the tensor's edges by itself, or rows x cols elements
-// where the pitch rules a tensor map out (4096 x 4096 x 4095, GELU with z and
-// residual: 269 us element by element). Before the box is written again:
+// where the pitch rules a tensor map out. Before the box is written again:
 // box_free().
 RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, long long ld, int row0, int col0, int rows,
                           int cols, int vec, int lane) {
@@ -590,22 +620,7 @@ RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, l
     }
   } else {
     __syncwarp();
-    // eight lanes per row: the aligned 16-byte pieces inside it, then the
-    // elements before the first (up to 7) and behind the last
-    const int l = lane & 7;
-#pragma unroll 1
-    for (int r = lane >> 3; r < rows; r += 4) {
-      uint16_t* p = out + (row0 + r) * ld + col0;
-      const int head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2, from = head + 8 * l;
-      const int tail = cols < head ? cols : head + ((cols - head) & ~7);
-      if (from + 8 <= cols) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(box_at(box, r, l));
-        const uint4 hi = *reinterpret_cast<const uint4*>(box_at(box, r, (l + 1) & 7));
-        *reinterpret_cast<uint4*>(p + from) = shift16(lo, hi, 2 * head);
-      }
-      if (l < head && l < cols) p[l] = *box_elem(box, r, l);
-      if (tail + l < cols) p[tail + l] = *box_elem(box, r, tail + l);
-    }
+    box_store_pieces(box, out + row0 * ld + col0, ld, rows, cols, lane);
   }
 }
 RNX_DEVICE void box_free(int lane) {
@@ -796,6 +811,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int row0 = mt * kPairM + 128 * (int)rank + qd * 32;
       const int rows = min(32, q.M - row0);        // <= 0: none of this warp's rows exist
       bool gone = false;
+      if (ep.residual && !ep.vec && lane < rows) { // loaded late, in batches: into L2 beside the products
+        const uint16_t* r = ep.residual + (row0 + lane) * ep.ldr;
+        const int c0 = nt * p.bn + half * ch, c1 = min(q.N, c0 + half);
+        for (int c = c0; c < c1; c += 64) l2_prefetch(r + c);
+        if (c0 < c1) l2_prefetch(r + c1 - 1);
+      }
       for (int c = 0; c < chunks; ++c) {
         const int col0 = nt * p.bn + half * ch + 64 * c, cols = min(64, q.N - col0);
         BoxLoad res;
@@ -1146,27 +1167,55 @@ SplitPlan plan_split(const Product* prod, int n) {
         sum += us * t / tiles;
       }
       const long long waves = ceil_div(tiles * S, cap);
-      const double us = 0.9 + (waves == 1 ? longest : waves * sum);
+      const double us = 0.9 + (waves == 1 ? longest : std::max(longest, waves * sum));
       if (best.us < 0 || us < best.us) best = SplitPlan{us, S, {bn[0], bn[1]}};
     }
   }
   return best;
 }
 
-// A round of the pair kernel takes the longer of its products and its epilogue;
+// How the pairs share two products' tiles: each pair takes `rounds1` tiles of
+// the second behind its own of the first, then those with a tile less of the
+// first (from first_light on) go on alone. cost: of a tile; `end` in its units.
+struct PairSchedule {
+  double end;
+  int rounds1, first_light;
+};
+PairSchedule schedule_pairs(const long long* tiles, const double* cost, int pairs) {
+  const long long each = tiles[0] / pairs, heavy = tiles[0] % pairs, light = pairs - heavy;
+  PairSchedule best{-1, 0, (int)heavy};
+  auto end_of = [&](long long q) {
+    const long long rest = std::max<long long>(0, tiles[1] - q * pairs);
+    return std::max((each + (heavy > 0)) * cost[0] + q * cost[1],
+                    each * cost[0] + (q + ceil_div(rest, light)) * cost[1]);
+  };
+  // all end together at about this q: light pairs make up for a tile of the first
+  const long long most = ceil_div(tiles[1], pairs);
+  const double at = cost[1] > 0 ? ((double)tiles[1] - light * cost[0] / cost[1]) / pairs : 0;
+  const long long mid = at <= 0 ? 0 : std::min(most, (long long)at);
+  for (long long q = std::max<long long>(0, mid - 2); q <= std::min(most, mid + 2); ++q) {
+    const double end = end_of(q);
+    if (best.end < 0 || end < best.end) best.end = end, best.rounds1 = (int)q;
+  }
+  return best;
+}
+
+// A tile of the pair kernel takes the longer of its products and its epilogue;
 // a step takes longer the more pairs are at work (L2 and power).
+double pair_tile_us(const Product& q, int bn, double busy) {
+  const double step_us = bn == 256 ? 0.28 + 0.09 * busy : 0.215 + 0.05 * busy;
+  const bool maps = q.ep.vec && q.b.rows % 8 == 0;           // stored by tensor maps
+  return std::max(ceil_div(q.red, kStepK) * step_us, bn == 256 ? (maps ? 2.4 : 4.5) : (maps ? 1.4 : 2.5));
+}
 double pair_us(const Product* prod, int n, int bn) {
   constexpr int kPairs = kNumSMs / 2;
-  long long tiles = 0;
-  for (int i = 0; i < n; ++i) tiles += ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
-  const long long rounds = ceil_div(tiles, kPairs);
-  const double busy = (double)tiles / (rounds * kPairs);
-  const double step_us = bn == 256 ? 0.28 + 0.09 * busy : 0.215 + 0.05 * busy;
-  double sum = 0;
-  for (int i = 0; i < n; ++i)
-    sum += (double)(ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn)) *
-           std::max(ceil_div(prod[i].red, kStepK) * step_us, bn == 256 ? 2.4 : 1.4);
-  return (bn == 256 ? 8.1 : 6.5) + rounds * (sum / tiles) + 0.5 * (rounds - 1);
+  long long tiles[2] = {0, 0};
+  for (int i = 0; i < n; ++i) tiles[i] = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
+  const long long all = tiles[0] + tiles[1], rounds = ceil_div(all, kPairs);
+  const double busy = (double)all / (rounds * kPairs);
+  double cost[2] = {0, 0};
+  for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, busy);
+  return (bn == 256 ? 8.1 : 6.5) + schedule_pairs(tiles, cost, kPairs).end + 0.5 * (rounds - 1);
 }
 
 struct Choice {
@@ -1278,20 +1327,11 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
   p.status = status;
   p.clear = clear;
   const int pairs = (int)std::min<long long>(kPairs, std::max<long long>(tiles[0], tiles[1]));
-  // second product: how many rounds all pairs share before those with a tile
-  // less of the first product go on alone, for the earliest end
-  const long long each = p.tiles0 / pairs, heavy = p.tiles0 % pairs;
-  const long long k0 = p.prob[0].ksteps, k1 = p.prob[1].ksteps;
-  p.first_light = (int)heavy;
-  long long best = -1;
-  for (long long q = 0; q <= (tiles[1] + pairs - 1) / pairs; ++q) {
-    const long long rest = std::max<long long>(0, tiles[1] - q * pairs), light = pairs - heavy;
-    const long long end = std::max((each + (heavy > 0)) * k0 + q * k1, each * k0 + (q + (rest + light - 1) / light) * k1);
-    if (best < 0 || end < best) {
-      best = end;
-      p.rounds1 = (int)q;
-    }
-  }
+  double cost[2] = {0, 0};
+  for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, 1);
+  const PairSchedule plan = schedule_pairs(tiles, cost, pairs);
+  p.rounds1 = plan.rounds1;
+  p.first_light = plan.first_light;
   switch (act) {
     case MOE_ACT_NONE: return launch_pair_act<MOE_ACT_NONE>(p, pairs, st);
     case MOE_ACT_RELU: return launch_pair_act<MOE_ACT_RELU>(p, pairs, st);
@@ -1477,11 +1517,13 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     return err;
   };
   if (n) {
-    // both in one launch, or one launch each where one wants the other kernel
+    // both in one launch, or one launch each where that is estimated shorter:
+    // a single form of tiles and splits hardly fits reductions of very different
+    // lengths (T 1, 1472 -> 5760: 33 us in one launch)
     const Choice both = choose(prod, n);
     if (n == 2) {
       const Choice first = choose(prod, 1), second = choose(prod + 1, 1);
-      if (!first.width != !second.width && first.us + second.us < both.us) {
+      if (first.us + second.us < both.us) {
         if ((e = launch(prod, 1, first)) != cudaSuccess) return e;
         if ((e = launch(prod + 1, 1, second)) != cudaSuccess) return e;
         n = 0;
@@ -1489,7 +1531,7 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     }
     if (n && (e = launch(prod, n, both)) != cudaSuccess) return e;
   }
-  if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 7) / 8), dim3(32), 0, st, db);
+  if (db.db) return launch_pdl(linear_db_kernel, dim3((a.N + 31) / 32), dim3(32), 0, st, db);
   return cudaSuccess;
 }
 
