@@ -134,38 +134,57 @@ RNX_DEVICE void fill_slot(float* slot, const float* logits, const int32_t* ids, 
   }
 }
 
-// Sums of the rows [lo, hi) by the whole CTA: normalised scores into
-// sums[0 .. E) (fixed order: rows within a lane group, then the groups of a
-// warp, then the warps) and assignment counts into hist[0 .. E). warp_sums:
-// kSumWarps * E floats. All threads call it; the results are published by its
-// last barrier.
+// A CTA's consecutive rows on their way through its rings: lane group j of warp
+// w takes rows first + (w + 16 n) 32 / G + j. It runs on from one sequence to the
+// next (starting anew at each cost 1 to 3 us of latency).
 template <int G, int NQ>
-RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, int lo, int hi, float* rings,
-                         float* warp_sums, int* hist) {
+struct RowStream {
+  static constexpr int R = 32 / G, STEP = kSumWarps * R, DEPTH = ring_depth<G, NQ>();
+  const float* logits;
+  const int32_t* ids;
+  float* ring;
+  int E, k, end, base, at;    // base: first row of the warp's present group (warp-uniform), in slot `at`
+  bool landed;
+
+  RNX_DEVICE void fill(int d, int first) {
+    const int lane = threadIdx.x & 31;
+    // a lane group without a row left reads the last one again and adds nothing
+    if (first < end) fill_slot<G, NQ>(ring + d * slot_floats(E, false), logits, ids, nullptr, E, k, min(first + lane / G, end - 1), lane % G);
+    cp_commit();
+  }
+  RNX_DEVICE void start(const float* logits_, const int32_t* ids_, int E_, int k_, int first, int end_, float* rings) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    logits = logits_, ids = ids_, E = E_, k = k_, end = end_;
+    ring = rings + (size_t)(warp * R + lane / G) * DEPTH * slot_floats(E, false);
+    base = first + warp * R;
+    at = 0;
+    landed = false;
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fill(d, base + d * STEP);
+  }
+};
+
+// Sums of the rows [lo, hi) of a stream by the whole CTA: normalised scores into
+// sums[0 .. E) (fixed order: rows within a lane group, then the groups of a
+// warp, then the warps) and assignment counts added to hist[0 .. E), which is
+// zero and published before. warp_sums: kSumWarps * E floats. All threads call
+// it; behind it thread t owns columns t + 512 i of both.
+template <int G, int NQ>
+RNX_DEVICE void sum_rows(RowStream<G, NQ>& st, int lo, int hi, float* warp_sums, int* hist) {
   constexpr int R = 32 / G, STEP = kSumWarps * R, DEPTH = ring_depth<G, NQ>();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane % G;
-  const int slot = slot_floats(E, false);
-  float* ring = rings + (size_t)(warp * R + lane / G) * DEPTH * slot;
-  for (int e = tid; e < E; e += kSumWarps * 32) hist[e] = 0;
-  int base = lo + warp * R;                              // the warp's first row (warp-uniform)
-  const int mine = lane / G;
-  // a lane group without a row left reads the last one again and adds nothing
-  auto fill = [&](int d, int first) {
-    if (first < hi) fill_slot<G, NQ>(ring + d * slot, logits, ids, nullptr, E, k, min(first + mine, hi - 1), g);
-    cp_commit();
-  };
-#pragma unroll
-  for (int d = 0; d < DEPTH - 1; ++d) fill(d, base + d * STEP);
-  __syncthreads();
+  const int E = st.E, k = st.k, slot = slot_floats(E, false), mine = lane / G;
   float acc[4 * NQ];
 #pragma unroll
   for (int i = 0; i < 4 * NQ; ++i) acc[i] = 0.f;
-  for (int at = 0; base < hi; base += STEP, at = at == DEPTH - 1 ? 0 : at + 1) {
-    __syncwarp();                                        // the slot filled now was read one row ago
-    fill(at == 0 ? DEPTH - 1 : at - 1, base + (DEPTH - 1) * STEP);
-    cp_wait<DEPTH - 1>();
-    __syncwarp();
-    const float* src = ring + at * slot;
+  while (st.base < hi) {
+    if (!st.landed) {
+      __syncwarp();                                      // the slot filled now was read one row ago
+      st.fill(st.at == 0 ? DEPTH - 1 : st.at - 1, st.base + (DEPTH - 1) * STEP);
+      cp_wait<DEPTH - 1>();
+      __syncwarp();
+    }
+    const float* src = st.ring + st.at * slot;
     float s[4 * NQ], total = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -181,7 +200,14 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
       }
     }
     total = row_sum<G>(total);
-    const bool exists = base + mine < hi;
+    const int row = st.base + mine;
+    const bool exists = row >= lo && row < hi;
+    if (st.base < lo || st.base + R > hi) {              // warp-uniform: rows of another sequence, NaN included
+      if (!exists) {
+#pragma unroll
+        for (int i = 0; i < 4 * NQ; ++i) s[i] = 0.f;
+      }
+    }
     const float inv = total == 0.f || !exists ? 0.f : 1.0f / total;      // a row of zero scores has no shares
 #pragma unroll
     for (int i = 0; i < 4 * NQ; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
@@ -189,8 +215,11 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
       const int id = __float_as_int(src[padded(E) + j]);
       if (exists && id >= 0 && id < E) atomicAdd(hist + id, 1);          // integer: the order does not matter
     }
+    st.landed = st.base + R > hi && hi < st.end;         // the next sequence takes the rest of this group
+    if (st.landed) break;
+    st.base += STEP;
+    st.at = st.at == DEPTH - 1 ? 0 : st.at + 1;
   }
-  cp_wait<0>();
 #pragma unroll
   for (int i = 0; i < 4 * NQ; ++i) {
 #pragma unroll
@@ -205,6 +234,9 @@ RNX_DEVICE void sum_rows(const float* logits, const int32_t* ids, int E, int k, 
     for (int w = 0; w < kSumWarps; ++w) v += warp_sums[w * E + e];
     warp_sums[e] = v;                                    // only this thread reads or writes column e
   }
+}
+RNX_DEVICE void clear_counts(int* hist, int E) {
+  for (int e = threadIdx.x; e < E; e += kSumWarps * 32) hist[e] = 0;
   __syncthreads();
 }
 
@@ -263,7 +295,12 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_seq_kernel(const Ba
   pdl_wait();
   pdl_trigger();
   const int lo = seq_start(p.off, b, p.T), hi = max(lo, seq_start(p.off, b + 1, p.T));
-  sum_rows<G, NQ>(p.logits, p.ids, p.E, p.k, lo, hi, dyn, warp_sums, hist);
+  RowStream<G, NQ> rows;
+  rows.start(p.logits, p.ids, p.E, p.k, lo, hi, dyn);
+  clear_counts(hist, p.E);
+  sum_rows(rows, lo, hi, warp_sums, hist);
+  cp_wait<0>();
+  __syncthreads();
   finish_sequence(warp_sums, hist, p.E, p.k, hi - lo, p.coef, p.counts + (size_t)b * p.E, p.mean + (size_t)b * p.E,
                   p.loss + b, red);
 }
@@ -280,19 +317,24 @@ __global__ void __launch_bounds__(kSumWarps * 32, 1) balance_partial_kernel(cons
   pdl_trigger();
   const int r0 = (int)min((long long)blockIdx.x * p.rows_per_block, (long long)p.T);
   const int r1 = (int)min((long long)r0 + p.rows_per_block, (long long)p.T);
+  RowStream<G, NQ> rows;
+  rows.start(p.logits, p.ids, p.E, p.k, r0, r1, dyn);      // its latency beside the search
+  clear_counts(hist, p.E);
   for (int b = seq_of_row(p.off, p.B, p.T, r0); b < p.B; ++b) {
     const int start = seq_start(p.off, b, p.T);
     if (start >= r1) break;
     const int lo = max(r0, start), hi = min(r1, seq_start(p.off, b + 1, p.T));
     if (lo >= hi) continue;
-    sum_rows<G, NQ>(p.logits, p.ids, p.E, p.k, lo, hi, dyn, warp_sums, hist);
+    sum_rows(rows, lo, hi, warp_sums, hist);
     const size_t slot = (size_t)(blockIdx.x + b) * p.E;
-    for (int e = threadIdx.x; e < p.E; e += kSumWarps * 32) {
+    for (int e = threadIdx.x; e < p.E; e += kSumWarps * 32) {   // as sum_rows left them to the threads
       p.psum[slot + e] = warp_sums[e];
       p.pcnt[slot + e] = hist[e];
+      hist[e] = 0;
     }
     __syncthreads();
   }
+  cp_wait<0>();
 }
 
 // Step 2: one CTA per sequence adds its slots in order. Warps split the slots

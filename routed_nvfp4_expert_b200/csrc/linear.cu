@@ -648,7 +648,7 @@ RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
   __syncwarp();
 }
 // The same from rows on any element, straight into the box. `end`: the matrix's.
-constexpr int kBoxRows = 4;
+constexpr int kBoxRows = 2;
 RNX_DEVICE void box_load_any(uint8_t* box, const uint16_t* src, long long ld, int rows, int cols, const uint16_t* end,
                              int lane) {
   const int c = lane & 7;
