@@ -589,26 +589,28 @@ RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
 // behind the last. (4096 x 640 -> 4691 with residual: 215 us by elements, 64 us
 // by pieces; words of two columns, for even pitches, gain 5% without a residual
 // and lose 11% with one.)
+template <int UNROLL>
 RNX_DEVICE void box_store_pieces(uint8_t* box, uint16_t* out, long long ld, int rows, int cols, int lane) {
   const int l = lane & 7;
-#pragma unroll 1
-  for (int r = lane >> 3; r < rows; r += 4) {
-    uint16_t* p = out + r * ld;
+  uint16_t* p = out + (lane >> 3) * ld;
+#pragma unroll UNROLL
+  for (int r = lane >> 3; r < rows; r += 4, p += 4 * ld) {
     const int head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2, from = head + 8 * l;
-    const int tail = cols < head ? cols : head + ((cols - head) & ~7);
-    if (from + 8 <= cols) {
-      const uint4 lo = *reinterpret_cast<const uint4*>(box_at(box, r, l));
-      const uint4 hi = *reinterpret_cast<const uint4*>(box_at(box, r, (l + 1) & 7));
-      *reinterpret_cast<uint4*>(p + from) = shift16(lo, hi, 2 * head);
-    }
-    if (l < head && l < cols) p[l] = *box_elem(box, r, l);
-    if (tail + l < cols) p[tail + l] = *box_elem(box, r, tail + l);
+    const int tail = (cols < head ? cols : head + ((cols - head) & ~7)) + l;
+    const uint4 piece = shift16(*reinterpret_cast<const uint4*>(box_at(box, r, l)),
+                                *reinterpret_cast<const uint4*>(box_at(box, r, (l + 1) & 7)), 2 * head);
+    const uint16_t before = *box_elem(box, r, l), behind = *box_elem(box, r, min(tail, 63));
+    if (from + 8 <= cols) *reinterpret_cast<uint4*>(p + from) = piece;
+    if (l < head && l < cols) p[l] = before;
+    if (tail < cols) p[tail] = behind;
   }
 }
+
 // The box to global memory at column col0, row row0 (whole warp): one tensor
 // store, which ends at the tensor's edges by itself, or rows x cols elements
 // where the pitch rules a tensor map out. Before the box is written again:
 // box_free().
+template <int UNROLL>
 RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, long long ld, int row0, int col0, int rows,
                           int cols, int vec, int lane) {
   if (vec) {
@@ -620,7 +622,7 @@ RNX_DEVICE void box_store(uint8_t* box, const CUtensorMap* map, uint16_t* out, l
     }
   } else {
     __syncwarp();
-    box_store_pieces(box, out + row0 * ld + col0, ld, rows, cols, lane);
+    box_store_pieces<UNROLL>(box, out + row0 * ld + col0, ld, rows, cols, lane);
   }
 }
 RNX_DEVICE void box_free(int lane) {
@@ -648,7 +650,7 @@ RNX_DEVICE void box_land(const BoxLoad& b, uint8_t* box, int lane) {
   __syncwarp();
 }
 // The same from rows on any element, straight into the box. `end`: the matrix's.
-constexpr int kBoxRows = 2;
+constexpr int kBoxRows = 2, kBoxUnroll = 2;
 RNX_DEVICE void box_load_any(uint8_t* box, const uint16_t* src, long long ld, int rows, int cols, const uint16_t* end,
                              int lane) {
   const int c = lane & 7;
@@ -869,7 +871,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                            pack2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
                            pack2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
                            pack2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
-          box_store(box, &q.tma_z, ep.z, ep.ldz, row0, col0, rows, cols, ep.vec, lane);
+          box_store<1>(box, &q.tma_z, ep.z, ep.ldz, row0, col0, rows, cols, ep.vec, lane);
           box_free(lane);
         }
         if (res_src) {
@@ -894,7 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           *at = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
                            pack2(y[6], y[7]));
         }
-        box_store(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
+        box_store<kBoxUnroll>(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
       }
       if (gone) {
         if (lane == 0) {
@@ -1200,22 +1202,34 @@ PairSchedule schedule_pairs(const long long* tiles, const double* cost, int pair
   return best;
 }
 
-// A tile of the pair kernel takes the longer of its products and its epilogue;
-// a step takes longer the more pairs are at work (L2 and power).
-double pair_tile_us(const Product& q, int bn, double busy) {
+// A tile of the pair kernel: its products (a step takes longer the more pairs
+// are at work: L2 and power) and its epilogue, which run beside each other.
+struct PairTileUs {
+  double mma, all;
+};
+PairTileUs pair_tile_us(const Product& q, int bn, double busy) {
   const double step_us = bn == 256 ? 0.28 + 0.09 * busy : 0.215 + 0.05 * busy;
   const bool maps = q.ep.vec && q.b.rows % 8 == 0;           // stored by tensor maps
-  return std::max(ceil_div(q.red, kStepK) * step_us, bn == 256 ? (maps ? 2.4 : 4.5) : (maps ? 1.4 : 2.5));
+  const double mma = ceil_div(q.red, kStepK) * step_us + 0.5;
+  return {mma, std::max(mma, bn == 256 ? (maps ? 2.5 : 4.5) : (maps ? 1.5 : 2.5))};
 }
 double pair_us(const Product* prod, int n, int bn) {
   constexpr int kPairs = kNumSMs / 2;
-  long long tiles[2] = {0, 0};
-  for (int i = 0; i < n; ++i) tiles[i] = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
-  const long long all = tiles[0] + tiles[1], rounds = ceil_div(all, kPairs);
-  const double busy = (double)all / (rounds * kPairs);
-  double cost[2] = {0, 0};
-  for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, busy);
-  return (bn == 256 ? 8.1 : 6.5) + schedule_pairs(tiles, cost, kPairs).end + 0.5 * (rounds - 1);
+  long long tiles[2] = {0, 0}, steps = 0;
+  for (int i = 0; i < n; ++i) {
+    tiles[i] = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
+    steps = std::max(steps, ceil_div(prod[i].red, kStepK));
+  }
+  const long long all = tiles[0] + tiles[1];
+  const double busy = (double)all / (ceil_div(all, kPairs) * kPairs);
+  double mma[2] = {0, 0}, cost[2] = {0, 0};
+  for (int i = 0; i < n; ++i) {
+    const PairTileUs t = pair_tile_us(prod[i], bn, busy);
+    mma[i] = t.mma, cost[i] = t.all;
+  }
+  // filling and draining the pipeline costs less where a tile is a step or two
+  const double ends = std::min(bn == 256 ? 7.6 : 6.0, 3.0 + 1.7 * steps);
+  return std::max(ends + schedule_pairs(tiles, mma, kPairs).end, 3.0 + schedule_pairs(tiles, cost, kPairs).end);
 }
 
 struct Choice {
@@ -1328,7 +1342,7 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
   p.clear = clear;
   const int pairs = (int)std::min<long long>(kPairs, std::max<long long>(tiles[0], tiles[1]));
   double cost[2] = {0, 0};
-  for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, 1);
+  for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, 1).all;
   const PairSchedule plan = schedule_pairs(tiles, cost, pairs);
   p.rounds1 = plan.rounds1;
   p.first_light = plan.first_light;
@@ -1517,13 +1531,14 @@ cudaError_t launch_linear_backward(int act, const LinearBackwardArgs& a, void* w
     return err;
   };
   if (n) {
-    // both in one launch, or one launch each where that is estimated shorter:
-    // a single form of tiles and splits hardly fits reductions of very different
-    // lengths (T 1, 1472 -> 5760: 33 us in one launch)
+    // both in one launch, or one launch each where that is estimated a quarter
+    // shorter (the second waits for the first's end): a single form of tiles and
+    // splits does not fit every pair of reductions. T 1, 1472 -> 5760: 40 us in
+    // one launch, 19 in two; T 64, 4096 -> 4096: 30 and 36.
     const Choice both = choose(prod, n);
     if (n == 2) {
       const Choice first = choose(prod, 1), second = choose(prod + 1, 1);
-      if (first.us + second.us < both.us) {
+      if (1.25 * (first.us + second.us) < both.us) {
         if ((e = launch(prod, 1, first)) != cudaSuccess) return e;
         if ((e = launch(prod + 1, 1, second)) != cudaSuccess) return e;
         n = 0;
