@@ -139,11 +139,6 @@ RNX_DEVICE void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uin
       : "memory");
 }
 
-// Bring a tensor map (a kernel parameter) into the copy engine's cache.
-RNX_DEVICE void tma_prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 // 2D tiled store of the box at (x, y) from shared memory (the layout the
 // tensor map's swizzle describes), tracked by the thread's bulk async-group.
 // Rows or columns outside the tensor are not written.
