@@ -33,7 +33,7 @@ namespace {
 // next tile's products, and the dz pass as many as it streams, so their
 // instruction count matters: with normcdff, tanhf, expf and full divisions the
 // epilogue took longer than the products (60% of the tensor pipe at 4096 x 4096
-// x 12288, 82% now) and the dz pass 3.3 times its HBM time. Everything is put
+// x 12288, 85% now) and the dz pass 3.3 times its HBM time (now 1.5). Everything is put
 // on one power of two and one reciprocal (within 2^-22 each); GELU takes erfc
 // from Abramowitz and Stegun 7.1.26 (absolute error 1.5e-7). All stay within
 // 2^-20 of 1 + |z|, far inside a bf16 step. With E = 2^(-v log2 e) and s = 1 /
@@ -586,7 +586,7 @@ RNX_DEVICE uint16_t* box_elem(uint8_t* box, int row, int col) {
 
 // A box to rows that no tensor map describes: eight lanes per row, the aligned
 // 16-byte pieces inside it, then the elements before the first (up to 7) and
-// behind the last. (4096 x 640 -> 4691 with residual: 215 us by elements, 64 us
+// behind the last. (4096 x 640 -> 4691 with residual: 215 us by elements, 58 us
 // by pieces; words of two columns, for even pitches, gain 5% without a residual
 // and lose 11% with one.)
 template <int UNROLL>
