@@ -310,3 +310,45 @@ def test_after_the_router():
     cnt, m, l, _, _ = _reference(logits.cpu(), ids.cpu(), [0, T], E, k, 0.01)
     assert torch.equal(counts.cpu().long(), cnt) and int(counts.sum()) == T * k
     assert np.allclose(loss.cpu().numpy(), l.numpy(), rtol=(T + 2 * E + 64) * U, atol=0)
+
+
+@pytest.mark.parametrize("E", [16, 64, 288, 384])
+@pytest.mark.parametrize("T", [700, 5000])
+def test_rows_of_a_neighbour_never_enter_a_sequence(E, T):
+    """Sequences that end inside a group of rows worked on together: NaN rows of
+    one, before the first and behind the last leave the others' results as they
+    are, to the bit."""
+    k = 4
+    cfg = capi.SiteConfig(4096, 1024, 1024, E, 0, E, k, 2.5, 7.0)
+    g = torch.Generator().manual_seed(E + T)
+    logits = torch.randn(T, E, generator=g).cuda()
+    ids = torch.randint(0, E, (T, k), generator=g).to(torch.int32).cuda()
+    off = [3, 3 + T // 5, 5 + T // 5, 6 + T // 5, T // 2 + 1, T - 9]
+    B = len(off) - 1
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+
+    def call(x):
+        counts = torch.full((B, E), -1, dtype=torch.int32, device="cuda")
+        mean, loss = torch.full((B, E), 7.0, device="cuda"), torch.full((B,), 7.0, device="cuda")
+        ws = capi.alloc_balance_workspace(cfg, T, B)
+        ws.fill_(0xFF)
+        capi.moe_balance_loss(cfg, x, ids, 0.01, counts, mean, loss, ws, seq_offsets=offsets)
+        return counts, mean, loss
+
+    bad = logits.clone()
+    bad[:off[0]] = float("nan")
+    bad[off[-1]:] = float("nan")
+    bad[off[1]:off[2]] = float("nan")
+    want, got = call(logits), call(bad)
+    assert torch.equal(got[0], want[0])
+    for b in range(B):
+        if b == 1:
+            assert got[1][b].isnan().all() and got[2][b].isnan()
+        else:
+            assert torch.equal(got[1][b], want[1][b]) and torch.equal(got[2][b], want[2][b])
+    share = logits.double().sigmoid()
+    share = share / share.sum(1, keepdim=True)
+    for b in range(B):
+        # sums of at most T terms of one sign in fp32, each within 2^-20 of its value
+        ref = share[off[b]:off[b + 1]].mean(0)
+        assert ((want[1][b].double() - ref).abs() <= (2.0 ** -20 + T * 2.0 ** -24) * ref).all()

@@ -251,6 +251,18 @@ def test_rows_on_every_element_boundary(T, K, N, extra):
     _check_backward(T, K, N, "silu", x, w, z, g, pitches=(1 + extra, 1 + (extra + 2) % 8, 1 + (extra + 5) % 8))
 
 
+@pytest.mark.parametrize("T,K,N,act", [
+    (1, 1472, 5760, "silu"), (1, 544, 5936, "none"), (16, 842, 5409, "gelu_tanh"), (275, 326, 2036, "none"),
+    (275, 328, 11040, "gelu"), (9706, 1344, 128, "relu"), (2, 4627, 2091, "silu"), (48, 1632, 2048, "gelu"),
+])
+def test_reductions_of_very_different_lengths(T, K, N, act):
+    """Few tokens or few features: dx and dW in launches of their own or sharing
+    one, and db joined by few CTAs."""
+    g = torch.Generator().manual_seed(T + K + N)
+    x, w = _rand(g, T, K), _rand(g, N, K, scale=K ** -0.5)
+    _check_backward(T, K, N, act, x, w, _rand(g, T, N, scale=1.5), g)
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_gradients_match_differences(act):
     """Directional differences of sum(dy * y) in 64 bits, through the forward's own kept z."""
