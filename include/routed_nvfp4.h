@@ -453,17 +453,26 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, cons
                               float* mean_scores, float* loss, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * Gradient of the logits from the routing weights of moe_router_topk
- * (d_weights) and from moe_balance_loss (d_loss), in one pass:
+ * Gradient of the logits from the routing weights (d_weights) and from
+ * moe_balance_loss (d_loss), in one pass. The weights are those normalised
+ * over the assignments that ids names,
+ *   w_tj = rsf s_tj / C_t,  C_t = the sum of the scores of token t's slots with
+ *                           an id in [0, E)
+ * which are moe_router_topk's with its ids unchanged:
  *   d_s_te  = d_loss[b] coef / (T_b S_t) (f_be - sum_j f_bj s_tj / S_t)
  *             + sum over slots j with ids[t, j] = e of
  *               rsf / C_t (d_weights[t, j] - sum_i d_weights[t, i] s_i / C_t)
  *   d_logits[t, e] = d_s_te s_te (1 - s_te)
- * where C_t is the sum of the chosen experts' scores. The counts carry no
- * gradient; selection (ids) is a constant.
- *   logits, ids, seq_offsets, num_seqs, coef: as for moe_balance_loss; ids
- *               outside [0, E) take no part
- *   d_weights   fp32 [T, k], NULL = no such term
+ * The counts carry no gradient; selection (ids) is a constant.
+ * Dropped assignments: where the kept ones' weights stay as they were, a
+ * dropped expert's score is still part of them, so pass the router's ids
+ * unchanged and d_weights 0 in its slot. An id outside [0, E) takes the slot
+ * out of C_t: use it only where the kept weights are normalised again without
+ * it. counts are an input of their own, so moe_balance_loss may be given marked
+ * ids in either case.
+ *   logits, ids, seq_offsets, num_seqs, coef: as for moe_balance_loss
+ *   d_weights   fp32 [T, k], NULL = no such term; slots with an id outside
+ *               [0, E) are not read into anything
  *   counts      int32 [num_seqs, E] of moe_balance_loss, d_loss fp32
  *               [num_seqs]; both NULL = no balance term
  *   d_logits    out fp32 [T, E], not overlapping the inputs; rows outside all

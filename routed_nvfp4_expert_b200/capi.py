@@ -434,7 +434,10 @@ def moe_balance_loss(cfg: SiteConfig, logits, ids, coef: float, counts, mean_sco
 def moe_router_backward(cfg: SiteConfig, logits, ids, d_logits, d_weights=None, coef: float = 0.0, counts=None,
                         d_loss=None, seq_offsets=None, stream=None):
     """Gradient of the logits from the routing weights (d_weights fp32 [T, k])
-    and the balance loss (counts of moe_balance_loss and d_loss fp32 [B])."""
+    and the balance loss (counts of moe_balance_loss and d_loss fp32 [B]). The
+    weights are those normalised over the ids in [0, E): for an assignment
+    dropped after moe_router_topk normalised them, keep its id and set its
+    d_weights to 0."""
     T, E, k, B = logits.shape[0], cfg.num_experts, cfg.top_k, _seqs(seq_offsets)
     dev, st = _device_and_stream(logits, stream)
     _check(lib().moe_router_backward(

@@ -8,7 +8,8 @@
 // f is a count and carries no gradient, so with g_b = d loss_b (upstream)
 //   d s_te = g_b coef / (T_b S_t) (f_be - sum_j f_bj s_tj / S_t)
 // and with the routing weights w_j = rsf s_j / C, C = sum over the token's
-// chosen experts, and upstream v_j = d w_j
+// slots with an id in [0, E) (one dropped after the weights were normalised
+// keeps its id and has v = 0), and upstream v_j = d w_j
 //   d s_(id_j) += rsf / C (v_j - sum_i v_i s_i / C)
 // and d l = d s * s (1 - s).
 //
