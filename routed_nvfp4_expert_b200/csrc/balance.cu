@@ -390,6 +390,14 @@ struct GradParams {
   float coef, rsf;
 };
 
+// Both means are sums of products with scores that may be as small as 2^-126,
+// divided by a sum of such scores: the other factor is raised by 2^40 for the
+// sum (exact; factors from 2^-40 to 2^87 keep their accuracy beside any
+// score) and lowered again behind the division. Every gradient is formed as
+// (slope / sum of scores) (upstream times difference): the first factor is at
+// most 1, while the sum's reciprocal alone reaches 2^126.
+constexpr float kRaise = 1099511627776.f, kLower = 1.f / kRaise;
+
 // G lanes per row, each warp a run of consecutive rows, so that the loads f of
 // its sequence stay in registers. The routing weights' part of a row is k
 // values: the row without them goes back to its slot, the slots' lanes add
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
   int b = seq_of_row(p.off, p.B, p.T, base);
   int start = b < p.B ? seq_start(p.off, b, p.T) : p.T, end = b < p.B ? seq_start(p.off, b + 1, p.T) : p.T;
   bool fresh = true;
-  float f[4 * NQ], gain = 0.f;
+  float f[4 * NQ], gain = 0.f;                   // f times 2^40, gain times 2^-40
 #pragma unroll
   for (int i = 0; i < 4 * NQ; ++i) f[i] = 0.f;
   for (int at = 0; base < r1; base += R, at = at == DEPTH - 1 ? 0 : at + 1) {
@@ -440,8 +448,8 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
     if (inside && fresh && p.d_loss) {
       fresh = false;
       const float n = (float)(end - start);
-      gain = p.d_loss[b] * p.coef / n;
-      const float fs = (float)E / ((float)k * n);
+      gain = p.d_loss[b] * p.coef / n * kLower;
+      const float fs = kRaise * ((float)E / ((float)k * n));
       const int32_t* count = p.counts + (size_t)b * E;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
@@ -475,14 +483,14 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
         slope[h] = id[h] >= 0 ? slope_of(sc[h], ex) : 0.f;
         v[h] = id[h] >= 0 ? src[tail + kMaxK + j] : 0.f;
         c += sc[h];
-        m = fmaf(v[h], sc[h], m);
+        m = fmaf(v[h], sc[h] * kRaise, m);
       }
       c = row_sum<G>(c);
       m = row_sum<G>(m);
       const float ic = c == 0.f ? 0.f : 1.0f / c;
-      m *= ic;
+      m *= ic * kLower;
 #pragma unroll
-      for (int h = 0; h < SL; ++h) d[h] = p.rsf * ic * (v[h] - m) * slope[h];
+      for (int h = 0; h < SL; ++h) d[h] = slope[h] * ic * (p.rsf * (v[h] - m));
       // An expert named in several slots gets their sum, in slot order, from
       // its first. Hardly ever: k ids in k lanes are compared with one match.
       bool twice = k > G;
@@ -533,9 +541,9 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
     total = row_sum<G>(total);
     dot = row_sum<G>(dot);
     const float inv = total == 0.f ? 0.f : 1.0f / total;
-    const float mean = dot * inv, scale = gain * inv;
+    const float mean = dot * inv;
 #pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) l[i] *= scale * (f[i] - mean);
+    for (int i = 0; i < 4 * NQ; ++i) l[i] = l[i] * inv * (gain * (f[i] - mean));
     if (p.d_weights) {
       __syncwarp();                              // the slot's logits have been read
 #pragma unroll

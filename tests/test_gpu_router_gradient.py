@@ -123,3 +123,49 @@ def test_assignments_left_out_before_the_weights_are_normalised(T, E, k):
     _, mag = _weight_gradient(logits, marked, v)
     assert ((out - want).abs() <= _tol(E, logits) * mag + 1e-40).all()
     assert not out[0].any()
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 40, 4), (3000, 96, 8), (50, 288, 8), (9, 700, 16)])
+@pytest.mark.parametrize("scale", [1e-8, 1.0, 1e5])
+def test_rows_of_very_low_scores(T, E, k, scale):
+    """Logits down to where a score just exceeds 2^-126 (l > -87.3), with small
+    and loss-scaled upstream gradients: no intermediate leaves the range, and
+    nothing is lost where the gradient itself is an ordinary number."""
+    g = torch.Generator().manual_seed(E)
+    logits = -75.0 - 12.2 * torch.rand(T, E, generator=g)
+    logits[1] = -87.0                                      # all equal: v - m alone decides
+    logits[2, : E // 2] = 3.0                              # ordinary scores beside the lowest
+    ids = torch.rand(T, E, generator=g).topk(k, dim=1).indices.to(torch.int32)
+    v = torch.randn(T, k, generator=g) * scale
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E).to(torch.int32)[None]
+    d_loss = torch.tensor([scale])
+    grad, mag = _weight_gradient(logits, ids, v)
+    bal, bal_mag = _loss_gradient(logits, counts, k, 0.5, d_loss)
+    tol = _tol(E, logits)
+    assert tol < 3e-4
+    out = _call(logits, ids, k, d_weights=v)
+    assert ((out - grad).abs() <= tol * mag + 1e-40).all()
+    out = _call(logits, ids, k, counts=counts, coef=0.5, d_loss=d_loss)
+    assert ((out - bal).abs() <= tol * bal_mag + 1e-40).all()
+    out = _call(logits, ids, k, d_weights=v, counts=counts, coef=0.5, d_loss=d_loss)
+    assert ((out - grad - bal).abs() <= tol * (mag + bal_mag) + 1e-40).all()
+
+
+def test_a_large_scaling_factor_at_the_lowest_scores():
+    """rsf / C beyond the range while every weight is rsf / k: slots of equal
+    upstream gradients have a gradient of 0 up to rounding, not NaN or infinity."""
+    T, E, k, rsf = 6, 32, 4, 1000.0
+    logits = torch.full((T, E), -87.2)
+    ids = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    cfg = capi.SiteConfig(256, 128, 0, E, 0, E, k, rsf, 7.0)
+    out = torch.empty(T, E, device="cuda")
+    v = torch.ones(T, k)
+    v[T // 2:, 0] = 3.0
+    capi.moe_router_backward(cfg, logits.cuda(), ids.cuda(), out, d_weights=v.cuda())
+    out = out.cpu().double()
+    # with equal scores, m = sum(v s) (1 / C) is off by its three sums, the products, the reciprocal and the last
+    # product: 8 u of |v| = 1, and a weight is rsf / 4
+    assert (out[:T // 2].abs() <= rsf / 4 * 8 * U).all()
+    # m = 1.5
+    want = rsf / 4 * (v.double() - v.double().mean(1, keepdim=True))
+    assert ((out[:, :k] - want).abs() <= 1e-5 * rsf).all() and not out[:, k:].any()
