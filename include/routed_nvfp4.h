@@ -506,8 +506,9 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GEL
  *   and outputs are not allowed.
  *   ws: linear_workspace_size(T, K, N, ldx, ldw) bytes (0 on invalid
  *   arguments), contents need no initialisation; its first 4 bytes are a
- *   device status word (moe_read_device_status). Calls that may overlap on the
- *   GPU need workspaces of their own.
+ *   device status word (moe_read_device_status), cleared by every call, one
+ *   without tokens included. Calls that may overlap on the GPU need workspaces
+ *   of their own.
  * The order of every sum is fixed: equal inputs give equal bits. A row's
  * result may depend on T in its last bit (the split of the reduction does).
  */

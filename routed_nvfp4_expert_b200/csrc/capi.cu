@@ -132,6 +132,12 @@ moe_status_t check_seqs(const int32_t* off, int32_t n, bool sizes_only) {
   return MOE_OK;
 }
 
+// A call without tokens launches nothing that would clear the status word of a
+// workspace that its caller may read next.
+cudaError_t clear_status(void* ws, size_t ws_bytes, cudaStream_t st) {
+  return ws && ws_bytes >= 4 ? cudaMemsetAsync(ws, 0, 4, st) : cudaSuccess;
+}
+
 // Row pitches stay below the tensor map's limit of 2^40 bytes.
 moe_status_t check_pitch(int64_t ld, int32_t cols, const char* name) {
   if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s=%lld is below the row length %d", name, (long long)ld, cols);
@@ -846,7 +852,10 @@ moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T,
                          void* stream) {
   moe_status_t s;
   if ((s = check_linear(act, T, K, N, ldx, ldw)) != MOE_OK) return s;
-  if (T == 0) return MOE_OK;
+  if (T == 0) {
+    RNX_CUDA(clear_status(ws, ws_bytes, (cudaStream_t)stream), "clear status");
+    return MOE_OK;
+  }
   RNX_PTR(x, "x");
   RNX_PTR(w, "w");
   RNX_PTR(y, "y");
@@ -888,6 +897,7 @@ moe_status_t linear_bf16_backward(int32_t act, const uint16_t* dy, int64_t lddy,
   if (T == 0) {
     if (dw) RNX_CUDA(cudaMemset2DAsync(dw, 2 * (size_t)lddw, 0, 2 * (size_t)K, N, st), "clear dw");
     if (db) RNX_CUDA(cudaMemsetAsync(db, 0, 4 * (size_t)N, st), "clear db");
+    RNX_CUDA(clear_status(ws, ws_bytes, st), "clear status");
     return MOE_OK;
   }
   RNX_PTR(dy, "dy");
