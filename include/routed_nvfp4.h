@@ -478,8 +478,8 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, cons
  *   d_logits    out fp32 [T, E], not overlapping the inputs; rows outside all
  *               sequences are left as they were
  * A zero score sum (S_t or C_t) gives zero for its term; in both calls a score
- * below 2^-126 counts as 0. At least one of
- * d_weights and d_loss is required. Needs no workspace.
+ * below 2^-126 counts as 0. At least one of d_weights and d_loss is required
+ * (unless T or num_seqs is 0, where they may be empty). Needs no workspace.
  */
 moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, const int32_t* ids, int32_t T,
                                  const float* d_weights, const int32_t* seq_offsets, int32_t num_seqs, float coef,
@@ -523,7 +523,7 @@ moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T,
  *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  db = sum_t dz
  *   dy bf16 [T, N]; z bf16 [T, N], the pre-activation linear_bf16 kept (NULL
  *   with MOE_ACT_NONE); dx bf16 [T, K], dw bf16 [N, K], db fp32 [N]: out, each
- *   may be NULL, not all. The residual's gradient is dy itself. dz enters the
+ *   may be NULL, not all (unless T = 0, where dx is empty). The residual's gradient is dy itself. dz enters the
  *   two products rounded to bf16 and db unrounded; accumulation is fp32.
  *   Pitches as above. T = 0 writes zeros to dw and db.
  *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above.

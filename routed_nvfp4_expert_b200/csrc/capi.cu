@@ -816,7 +816,9 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, c
       (s = check_seqs(seq_offsets, num_seqs, false)) != MOE_OK)
     return s;
   if (!std::isfinite(coef)) return fail(MOE_ERR_INVALID_ARG, "coef is not finite");
-  if (!d_weights && !d_loss) return fail(MOE_ERR_INVALID_ARG, "d_weights and d_loss are both NULL");
+  // an empty tensor's pointer may be NULL: without tokens or sequences nothing tells it from an absent one
+  if (T > 0 && num_seqs > 0 && !d_weights && !d_loss)
+    return fail(MOE_ERR_INVALID_ARG, "d_weights and d_loss are both NULL");
   if (!d_loss != !counts) return fail(MOE_ERR_INVALID_ARG, "d_loss and counts go together: one of them is NULL");
   if (T == 0 || num_seqs == 0) return MOE_OK;
   RNX_PTR(logits, "logits");
@@ -883,7 +885,8 @@ moe_status_t linear_bf16_backward(int32_t act, const uint16_t* dy, int64_t lddy,
                                   float* db, void* ws, size_t ws_bytes, void* stream) {
   moe_status_t s;
   if ((s = check_linear(act, T, K, N, ldx, ldw)) != MOE_OK) return s;
-  if (!dx && !dw && !db) return fail(MOE_ERR_INVALID_ARG, "dx, dw and db are all NULL");
+  // without tokens dx is empty and its pointer may be NULL
+  if (T > 0 && !dx && !dw && !db) return fail(MOE_ERR_INVALID_ARG, "dx, dw and db are all NULL");
   if (dx) {
     RNX_PTR(dx, "dx");
     if ((s = check_pitch(lddx, K, "lddx")) != MOE_OK) return s;
