@@ -441,7 +441,8 @@ moe_status_t nvfp4_dequant(const uint8_t* codes, const uint8_t* scales, const fl
  *               every access stays in bounds.
  *   counts int32 [num_seqs, E], mean_scores fp32 [num_seqs, E], loss fp32
  *   [num_seqs]: out.
- *   ws: moe_balance_workspace_size bytes, contents need no initialisation.
+ *   ws: moe_balance_workspace_size bytes, contents need no initialisation;
+ *   fewer tokens or sequences never need more.
  * A row whose scores sum to 0 adds nothing to mean_scores; a NaN logit makes
  * its sequence's mean_scores and loss NaN. All of the FULL expert count is
  * counted (local range ignored). T = 0 writes zeros. The order of every sum is
@@ -526,7 +527,8 @@ moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T,
  *   may be NULL, not all (unless T = 0, where dx is empty). The residual's gradient is dy itself. dz enters the
  *   two products rounded to bf16 and db unrounded; accumulation is fp32.
  *   Pitches as above. T = 0 writes zeros to dw and db.
- *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above.
+ *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above;
+ *   here and in linear_bf16 fewer tokens of the same pitches never need more.
  */
 size_t linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int64_t ldx, int64_t ldw);
 moe_status_t linear_bf16_backward(int32_t act, const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,

@@ -663,6 +663,10 @@ int balance_blocks(int T) {
   return (T + r - 1) / r;
 }
 
+int balance_scratch_blocks(int T) {
+  return T <= kBalanceSeqMaxT ? 0 : min(kNumSMs, (T + kSumWarps - 1) / kSumWarps);
+}
+
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
                                 cudaStream_t st) {

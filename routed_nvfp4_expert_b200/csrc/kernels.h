@@ -319,10 +319,13 @@ constexpr int kBalanceSeqMaxT = 128;
 // against 15.8 us; of 2048 x 288: 8.2 against 13.3 us). The host does not see
 // the lengths; were one sequence to hold all 2048 rows, it would take 47 us.
 constexpr int kBalanceManyMaxT = 2048, kBalanceManyMean = 64;
-// CTAs of the first step of launch_balance_loss (0: the one-launch form); its
-// scratch holds (blocks + B) * E floats and as many ints (also where many short
-// sequences leave it unused, so that fewer sequences never need more).
+// CTAs of the first step of launch_balance_loss (0: the one-launch form), and
+// the most of any up to T tokens. Its scratch holds (the most + B) * E floats and
+// as many ints, so that fewer tokens never need more (2368 make 148 CTAs, 2369
+// make 140), nor fewer sequences (it is there also where many short ones leave
+// it unused).
 int balance_blocks(int T);
+int balance_scratch_blocks(int T);
 // off: [B + 1] ascending row offsets (NULL with B = 1: all T rows).
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,

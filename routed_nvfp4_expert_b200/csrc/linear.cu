@@ -1412,6 +1412,11 @@ int dz_rows(int T, int N) {
   return (int)(round * rounds);
 }
 
+// The most chunks that dz_rows makes of any up to T rows: the chunks themselves
+// get fewer where T passes a limit (128 at T 4096, 65 at 4097), and a workspace
+// for T tokens has to do for fewer.
+size_t most_dz_chunks(int T) { return std::min<size_t>(128, (T + 8 * kDzRows - 1) / (8 * kDzRows)); }
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
@@ -1433,7 +1438,7 @@ LinearLayout linear_backward_layout(int T, int K, int N, long long ldx, long lon
   L.dz = o;
   o = up256(o + 2 * (size_t)T * copy_pitch(N));
   L.part = o;
-  if (T > 0) o = up256(o + 4 * (size_t)N * ((T + dz_rows(T, N) - 1) / dz_rows(T, N)));
+  o = up256(o + 4 * (size_t)N * most_dz_chunks(T));
   L.bytes = o;
   return L;
 }
