@@ -343,10 +343,11 @@ cudaError_t launch(const GemmParams& p, cudaStream_t st) {
 
 }  // namespace
 
-// Main-loop wait limit of the BF16 GEMM launches (the drain waits keep the
+// Main-loop wait limit of the BF16 products' launches (the drain waits keep the
 // default): kWaitLimitNs unless a test lowered it.
 static unsigned long long g_gemm_wait_ns = kWaitLimitNs;
 void set_test_wait_limit_ns(unsigned long long ns) { g_gemm_wait_ns = ns; }
+unsigned long long test_wait_limit_ns() { return g_gemm_wait_ns; }
 
 cudaError_t launch_bf16_gemm(bool gate_up, const uint16_t* a, int M, int K, const uint16_t* b0, const uint16_t* b1,
                              int N, float limit, uint16_t* out, uint32_t* status, cudaStream_t st, float* out_f32,

@@ -129,10 +129,11 @@ struct Ring {
 // Bounded wait of a whole warp. A producer's loop is part of a stage's round
 // trip (slot freed, copy issued, data, products, slot freed), and the ring
 // just covers that trip, so the common case is one try and one vote; the abort
-// flag is read only when the slot was not ready.
-RNX_DEVICE bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait_poll(bar, parity) && !*abort_flag);
+// flag is read only when the slot was not ready. limit_ns 0 gives up on a slot
+// that is not ready at once (a try may hold the thread until it is).
+RNX_DEVICE bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+  if (__all_sync(0xffffffffu, limit_ns ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_poll(bar, parity, limit_ns) && !*abort_flag);
 }
 
 // Waits (bounded) until the last `issued` copies of a producer that stopped at
@@ -248,12 +249,15 @@ RNX_DEVICE void join_db(const DbJoin& d, int unit, int units, int lane) {
 // ordering); tiles above kPushColumns leave the part in their own shared memory
 // for the others to read after an ordering barrier. (1 x 1024 x 1024: 3.8 us
 // sent, 4.3 us read; 128 x 4096 x 4096, 128 columns: 16.2 us sent, 13.3 us
-// read.) Up to two products share a
+// read.) A barrier that each thread arrives at behind its last store, and waits
+// for at its end, keeps every CTA until no peer has anything left to send it.
+// Up to two products share a
 // launch (dx and dW of few tokens); a reduction of fewer steps than S leaves
 // the last ranks without a part of their own.
 // Warps: 0 = TMA producer, 1 = MMA issuer, 2 = TMEM allocator, 3-7 = db join,
 // 4-7 = TMEM readers; all eight reduce and store. Every wait is bounded; a
-// timeout sets the status word, and the CTA still meets its cluster's barrier.
+// timeout sets the status word, and the CTA still sends its (unspecified) part
+// and meets its cluster's barriers.
 
 constexpr int kSplitThreads = 256;
 constexpr int kSplitMaxStages = 10;
@@ -276,6 +280,7 @@ struct SplitParams {
   int tiles;                  // of all products
   int S, tmem_cols;
   int clear;
+  unsigned long long wait_ns; // limit of the ring's waits (the others keep the default)
 };
 
 template <int ACT>
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     int issued = 0;
     bool ok = true;
     for (int ks = k_lo; ks < k_hi; ++ks, ++issued, r.next(stages)) {
-      if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
+      if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, p.wait_ns))) break;
       if (elect_one()) {
         uint8_t* sA = smem + (size_t)r.slot * stage_bytes;
         uint8_t* sB = sA + kABytes;
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     Ring r;
     bool ok = true;
     for (int ks = k_lo; ks < k_hi; ++ks, r.next(stages)) {
-      if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
+      if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, p.wait_ns))) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t so = (uint64_t)((uint32_t)(r.slot * stage_bytes) >> 4);
@@ -389,8 +394,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     join_db(p.db, (int)blockIdx.x * 5 + warp - 3, (int)gridDim.x * 5, lane);
   }
 
-  // the producer and the issuer are through: every copy has landed and every
-  // MMA is done, so the stages may hold parts (the peers' too, after the barrier)
+  // the producer and the issuer are through: every copy has been seen to land
+  // and every MMA to end, on their barriers, so the stages may hold parts. No
+  // peer stores into them before this CTA's threads, behind those waits, have
+  // arrived at the cluster's barrier; it need not order memory, since what the
+  // stores overwrite is complete.
   const int nj = min(bn, q.J - j0), per = (nj + S - 1) / S;
   float* part = reinterpret_cast<float*>(smem);            // push: [parts][per][128], else [nj][128]
   __syncthreads();
@@ -425,8 +433,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
   }
   __syncwarp();
+  bool complete = true;
   if (push) {
-    if (__any_sync(0xffffffffu, !mbar_wait_cluster(&parts_bar, 0)) && lane == 0) set_status(p.status, kDevErrTimeout);
+    if (S > 1) cluster_arrive_relaxed();                   // this thread has nothing left to send
+    complete = __all_sync(0xffffffffu, mbar_wait_cluster(&parts_bar, 0));
+    if (!complete && lane == 0) set_status(p.status, kDevErrTimeout);
   } else if (S > 1) {
     cluster_sync_all();
   }
@@ -495,7 +506,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     }
   }
   __syncwarp();
-  if (!push && S > 1) cluster_sync_relaxed();   // no CTA leaves while a peer may still read its part
+  if (S > 1) {   // no CTA leaves while a peer may still read its part, or send it one
+    if (!push) cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  // what was sent by then is on its way at most
+  if (!complete && !mbar_wait_cluster(&parts_bar, 0)) set_status(p.status, kDevErrTimeout);
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -737,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool two = is_a || half > 64;          // MN-major blocks are 64 wide
       const bool expects = is_a && rank == 0;
       for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
-        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag))) break;
+        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, kWaitLimitNs))) break;
         if (elect_one()) {
           uint8_t* dst = smem + r.slot * kPairStageBytes + (is_a ? 0 : kABytes);
           const uint32_t bar = mapa_shared(smem_u32(&full_bar[r.slot]), 0);
@@ -777,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t acc = tmem + 256u * b;
         for (int ks = 0; ks < ksteps; ++ks, r.next(kPairStages)) {
-          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag))) break;
+          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, kWaitLimitNs))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t so = (uint64_t)((uint32_t)(r.slot * kPairStageBytes) >> 4);
@@ -1288,6 +1304,7 @@ cudaError_t launch_split(int act, const Product* prod, int n, const SplitPlan& p
       return cudaErrorInvalidValue;
   }
   p.S = S;
+  p.wait_ns = test_wait_limit_ns();
   p.tiles = (int)tiles;
   p.db = db;
   p.status = status;

@@ -182,8 +182,12 @@ RNX_DEVICE void mbar_arrive_cluster(uint32_t cluster_addr) {
 }
 
 // The same without ordering memory: every thread of the cluster has arrived.
+// In two halves, so that a thread does not wait where it arrives.
+RNX_DEVICE void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+RNX_DEVICE void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 RNX_DEVICE void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive_relaxed();
+  cluster_wait();
 }
 
 // fp32 from a CTA of the cluster (shared::cluster address).
