@@ -530,6 +530,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // which one tensor store writes them (the lanes' own stores where the pitch or N
 // is no multiple of 8 elements).
 // Every wait is bounded. No TMA load uses cluster multicast.
+//
+// A wait that runs out stops both CTAs, and the four producers may stop at
+// different steps: a step that only some of them issued would leave its copies
+// on the way, to either CTA, with a barrier that never completes. So each
+// producer leaves its count of issued steps in the even CTA, and once everything has
+// stopped that CTA counts the missing bytes as if they had come and waits
+// for the rest (pair_drain); only then do the CTAs leave.
 
 constexpr int kPairM = 256;
 constexpr int kPairStages = 6;
@@ -562,6 +569,7 @@ struct PairParams {
                               // only pairs with fewer tiles of the first do (pairs >= first_light)
   int first_light;
   int clear;
+  unsigned long long wait_ns; // limit of the main-loop waits (the others keep the default)
 };
 
 // The i-th tile of a pair: first the first product's, round robin, then the
@@ -695,6 +703,28 @@ RNX_DEVICE void box_load_any(uint8_t* box, const uint16_t* src, long long ld, in
   __syncwarp();
 }
 
+// Ends the copies of a pair that stopped early (one warp of the even CTA, when no
+// producer issues any more and every MMA is done). issued: steps by A and B of the
+// even, then of the odd CTA. No producer is ahead of another by more than the
+// ring, since a slot is freed by the products of a step that all four issued.
+RNX_DEVICE void pair_drain(uint64_t* full_bar, const volatile int* issued, uint32_t b_bytes, uint32_t* status, int lane) {
+  int first = issued[0], last = issued[0];
+  for (int i = 1; i < 4; ++i) first = min(first, issued[i]), last = max(last, issued[i]);
+  if (lane == 0) {
+    for (int step = first; step < last; ++step) {
+      uint64_t* bar = &full_bar[step % kPairStages];
+      if (issued[0] <= step) mbar_arrive_expect_tx(bar, 2u * (kABytes + b_bytes));   // the one that announces the bytes
+      for (int i = 0; i < 4; ++i)
+        if (issued[i] <= step) mbar_complete_tx(bar, i % 2 ? b_bytes : (uint32_t)kABytes);
+    }
+  }
+  __syncwarp();
+  for (int step = max(0, last - kPairStages); step < last; ++step)
+    if (!mbar_wait(&full_bar[step % kPairStages], (uint32_t)(step / kPairStages) & 1u) && lane == 0)
+      set_status(status, kDevErrTimeout);
+  __syncwarp();
+}
+
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
@@ -703,10 +733,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t full_bar[kPairStages], empty_bar[kPairStages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag;              // of both CTAs: set in each by whoever stops
+  __shared__ volatile int s_issued[4];             // the even CTA's: steps by A and B of the even, then of the odd CTA
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag));
+  auto stop_pair = [&] {                           // one lane; before the closing cluster_sync_all
+    set_status(p.status, kDevErrTimeout);
+    st_cluster(mapa_shared(abort_at, 0), 1u);
+    st_cluster(mapa_shared(abort_at, 1), 1u);
+  };
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int half = p.bn / 2;                       // this CTA's rows of B
 
@@ -753,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool two = is_a || half > 64;          // MN-major blocks are 64 wide
       const bool expects = is_a && rank == 0;
       for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
-        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, kWaitLimitNs))) break;
+        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, p.wait_ns))) break;
         if (elect_one()) {
           uint8_t* dst = smem + r.slot * kPairStageBytes + (is_a ? 0 : kABytes);
           const uint32_t bar = mapa_shared(smem_u32(&full_bar[r.slot]), 0);
@@ -768,12 +805,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
-      set_status(p.status, kDevErrTimeout);
-      abort_flag = 1;
+    if (lane == 0) {
+      if (!ok) stop_pair();
+      st_cluster(mapa_shared(smem_u32(const_cast<int*>(&s_issued[2 * rank + !is_a])), 0), (uint32_t)issued);
     }
-    // the even CTA's full barriers count both CTAs' copies of A and B
-    if (rank == 0) ring_drain(full_bar, r, issued, kPairStages, p.status, lane);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0) {
@@ -789,11 +824,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
         const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;
         const int b = tc & 1, ksteps = q.ksteps;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u, p.wait_ns)))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256u * b;
         for (int ks = 0; ks < ksteps; ++ks, r.next(kPairStages)) {
-          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, kWaitLimitNs))) break;
+          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, p.wait_ns))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t so = (uint64_t)((uint32_t)(r.slot * kPairStageBytes) >> 4);
@@ -808,10 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (elect_one()) mma_commit_pair_mc(&acc_full[b], 0x3);
         __syncwarp();
       }
-      if (!ok && lane == 0) {
-        set_status(p.status, kDevErrTimeout);
-        abort_flag = 1;
-      }
+      if (!ok && lane == 0) stop_pair();
       if (elect_one()) mma_commit_pair_mc(&mma_done, 0x1);
       __syncwarp();
       if (!mbar_wait(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
@@ -847,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
         if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);
         if (c == 0) {
-          if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u) || abort_flag)) {
+          if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u, p.wait_ns) || abort_flag)) {
             gone = true;
             break;
           }
@@ -921,10 +953,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         box_store<kBoxUnroll>(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
       }
       if (gone) {
-        if (lane == 0) {
-          set_status(p.status, kDevErrTimeout);
-          abort_flag = 1;
-        }
+        if (lane == 0) stop_pair();
         break;
       }
     }
@@ -932,10 +961,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 
   // no CTA leaves (or frees TMEM) while the pair's MMAs or copies may still
-  // touch its shared or tensor memory
+  // touch its shared or tensor memory; without an abort the products have
+  // consumed every copy
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
+  if (abort_flag) {                                // the same in all threads of both CTAs
+    if (rank == 0 && warp == 0) pair_drain(full_bar, s_issued, (uint32_t)half * 128u, p.status, lane);
+    cluster_sync_all();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmemCols);
@@ -1269,9 +1303,19 @@ Choice choose(const Product* prod, int n) {
   return c;
 }
 
+// A kernel's first CTA clears the status word beside the others' work, which is
+// early enough for waits of seconds alone: under a test's limit it is cleared before.
+cudaError_t clear_ahead(bool& clear, uint32_t* status, cudaStream_t st) {
+  if (!clear || test_wait_limit_ns() == kWaitLimitNs) return cudaSuccess;
+  clear = false;
+  return cudaMemsetAsync(status, 0, 4, st);
+}
+
 // The products' columns are the split kernel's m side, their rows its j side.
 cudaError_t launch_split(int act, const Product* prod, int n, const SplitPlan& plan, const DbJoin& db,
                          uint32_t* status, bool clear, cudaStream_t st) {
+  const cudaError_t cleared = clear_ahead(clear, status, st);
+  if (cleared != cudaSuccess) return cleared;
   SplitParams p;
   memset(&p, 0, sizeof p);
   const int S = plan.S;
@@ -1329,6 +1373,8 @@ cudaError_t launch_pair_act(const PairParams& p, int pairs, cudaStream_t st) {
 
 cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoin& db, uint32_t* status, bool clear,
                         cudaStream_t st) {
+  const cudaError_t cleared = clear_ahead(clear, status, st);
+  if (cleared != cudaSuccess) return cleared;
   PairParams p;
   memset(&p, 0, sizeof p);
   constexpr int kPairs = kNumSMs / 2;
@@ -1359,6 +1405,7 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
   }
   p.tiles0 = (int)tiles[0];
   p.tiles1 = (int)tiles[1];
+  p.wait_ns = test_wait_limit_ns();
   p.bn = bn;
   p.db = db;
   p.status = status;

@@ -190,6 +190,11 @@ RNX_DEVICE void cluster_sync_relaxed() {
   cluster_wait();
 }
 
+// One word into a CTA of the cluster, visible there behind a cluster_sync_all.
+RNX_DEVICE void st_cluster(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 // fp32 from a CTA of the cluster (shared::cluster address).
 RNX_DEVICE float4 ld_cluster_f4(uint32_t cluster_addr) {
   float4 v;
@@ -226,11 +231,13 @@ RNX_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait (cluster-scope acquire) for a barrier that peer CTAs arrive on.
-RNX_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+// limit_ns 0: one try.
+RNX_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit_ns = kWaitLimitNs) {
+  if (limit_ns == 0) return mbar_try_wait_cluster(bar, parity);
   unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 255u) == 255u && globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    if ((i & 255u) == 255u && globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
 

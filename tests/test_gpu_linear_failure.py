@@ -54,3 +54,50 @@ def test_few_tokens_backward():
     ws = capi.alloc_linear_backward_workspace(dy, x, w)
     _fails_and_recovers(lambda: capi.linear_bf16_backward(dy, x, w, ws, z=z, act="gelu", dx=dx, dw=dw, db=db), ws,
                         [dx, dw, db])
+
+
+@pytest.mark.parametrize("T,K,N", [(2049, 4096, 1280), (600, 64, 6000), (4096, 12288, 700), (900, 130, 4097)])
+def test_many_tokens(T, K, N):
+    g = torch.Generator().manual_seed(T)
+    x, w, r = _rand(g, T, K), _rand(g, N, K), _rand(g, T, N)
+    y, z = torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda")
+    ws = capi.alloc_linear_workspace(x, w)
+    _fails_and_recovers(lambda: capi.linear_bf16(x, w, y, ws, act="gelu", residual=r, z=z), ws, [y, z])
+
+
+@pytest.mark.parametrize("T,K,N,act", [(777, 1000, 515, "silu"), (2048, 1024, 2048, "none"), (64, 4096, 1024, "gelu")])
+def test_many_tokens_backward(T, K, N, act):
+    g = torch.Generator().manual_seed(T)
+    x, w, dy, z = _rand(g, T, K), _rand(g, N, K), _rand(g, T, N), _rand(g, T, N)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = capi.alloc_linear_backward_workspace(dy, x, w)
+    _fails_and_recovers(lambda: capi.linear_bf16_backward(dy, x, w, ws, z=z if act != "none" else None, act=act, dx=dx,
+                                                          dw=dw), ws, [dx, dw])
+
+
+@pytest.mark.parametrize("limit", [300, 2000, 20000])
+def test_waits_that_run_out_somewhere(limit):
+    """Limits near the copies' latency (ns): the producers and the issuer of a
+    pair stop at different steps, in some runs or in all. Whatever the status,
+    the calls end and the next one is right."""
+    T, K, N = 2049, 4096, 1280
+    g = torch.Generator().manual_seed(limit)
+    x, w = _rand(g, T, K), _rand(g, N, K)
+    y = torch.empty(T, N, dtype=BF16, device="cuda")
+    ws = capi.alloc_linear_workspace(x, w)
+    capi.linear_bf16(x, w, y, ws)
+    want = y.clone()
+    for _ in range(5):
+        capi.moe_set_wait_limit(limit)
+        try:
+            capi.linear_bf16(x, w, y, ws)
+            try:
+                capi.moe_read_device_status(ws)
+                assert torch.equal(y, want)
+            except capi.MoEError as e:
+                assert e.status == 5
+        finally:
+            capi.moe_set_wait_limit(-1)
+        capi.linear_bf16(x, w, y, ws)
+        capi.moe_read_device_status(ws)
+        assert torch.equal(y, want)
