@@ -280,11 +280,14 @@ struct SplitParams {
   int tiles;                  // of all products
   int S, tmem_cols;
   int clear;
-  unsigned long long wait_ns; // limit of the ring's waits (the others keep the default)
+  unsigned long long wait_ns; // with LIMIT, of the ring's waits (the others keep the default)
 };
 
-template <int ACT>
+// LIMIT: for a test's limit on the waits, which is in the way of every step as a
+// parameter (T 777, 1000 -> 515 backward: 14.2 against 13.9 us).
+template <int ACT, bool LIMIT>
 __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __grid_constant__ SplitParams p) {
+  const unsigned long long wait_ns = LIMIT ? p.wait_ns : kWaitLimitNs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) uint64_t full_bar[kSplitMaxStages], empty_bar[kSplitMaxStages], mma_done, parts_bar;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     int issued = 0;
     bool ok = true;
     for (int ks = k_lo; ks < k_hi; ++ks, ++issued, r.next(stages)) {
-      if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, p.wait_ns))) break;
+      if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, wait_ns))) break;
       if (elect_one()) {
         uint8_t* sA = smem + (size_t)r.slot * stage_bytes;
         uint8_t* sB = sA + kABytes;
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
     Ring r;
     bool ok = true;
     for (int ks = k_lo; ks < k_hi; ++ks, r.next(stages)) {
-      if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, p.wait_ns))) break;
+      if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, wait_ns))) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t so = (uint64_t)((uint32_t)(r.slot * stage_bytes) >> 4);
@@ -534,8 +537,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // A wait that runs out stops both CTAs, and the four producers may stop at
 // different steps: a step that only some of them issued would leave its copies
 // on the way, to either CTA, with a barrier that never completes. So each
-// producer leaves its count of issued steps in the even CTA, and once everything has
-// stopped that CTA counts the missing bytes as if they had come and waits
+// producer leaves its count of issued steps, and once everything has stopped the
+// even CTA collects them, counts the missing bytes as if they had come and waits
 // for the rest (pair_drain); only then do the CTAs leave.
 
 constexpr int kPairM = 256;
@@ -569,7 +572,7 @@ struct PairParams {
                               // only pairs with fewer tiles of the first do (pairs >= first_light)
   int first_light;
   int clear;
-  unsigned long long wait_ns; // limit of the main-loop waits (the others keep the default)
+  unsigned long long wait_ns; // with LIMIT, of the main-loop waits (the others keep the default)
 };
 
 // The i-th tile of a pair: first the first product's, round robin, then the
@@ -725,16 +728,17 @@ RNX_DEVICE void pair_drain(uint64_t* full_bar, const volatile int* issued, uint3
   __syncwarp();
 }
 
-template <int ACT>
+template <int ACT, bool LIMIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
+  const unsigned long long wait_ns = LIMIT ? p.wait_ns : kWaitLimitNs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) uint64_t full_bar[kPairStages], empty_bar[kPairStages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int abort_flag;              // of both CTAs: set in each by whoever stops
-  __shared__ volatile int s_issued[4];             // the even CTA's: steps by A and B of the even, then of the odd CTA
+  __shared__ volatile int s_issued[4];             // steps by A and B of the even, then of the odd CTA: its own here
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -790,7 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool two = is_a || half > 64;          // MN-major blocks are 64 wide
       const bool expects = is_a && rank == 0;
       for (int ks = 0; ks < ksteps; ++ks, ++issued, r.next(kPairStages)) {
-        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, p.wait_ns))) break;
+        if (!(ok = ring_wait(&empty_bar[r.slot], r.parity ^ 1u, &abort_flag, wait_ns))) break;
         if (elect_one()) {
           uint8_t* dst = smem + r.slot * kPairStageBytes + (is_a ? 0 : kABytes);
           const uint32_t bar = mapa_shared(smem_u32(&full_bar[r.slot]), 0);
@@ -807,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     if (lane == 0) {
       if (!ok) stop_pair();
-      st_cluster(mapa_shared(smem_u32(const_cast<int*>(&s_issued[2 * rank + !is_a])), 0), (uint32_t)issued);
+      s_issued[2 * rank + !is_a] = issued;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -824,11 +828,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t dB0 = q.b_mn ? sdesc_mn_sw128(s0 + kABytes, kMnBlock) : sdesc_k_sw128(s0 + kABytes);
         const uint64_t stepA = q.a_mn ? 2048 >> 4 : 32 >> 4, stepB = q.b_mn ? 2048 >> 4 : 32 >> 4;
         const int b = tc & 1, ksteps = q.ksteps;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u, p.wait_ns)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[b], ((uint32_t)(tc >> 1) & 1u) ^ 1u, wait_ns)))) break;
         tc_fence_after();
         const uint32_t acc = tmem + 256u * b;
         for (int ks = 0; ks < ksteps; ++ks, r.next(kPairStages)) {
-          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, p.wait_ns))) break;
+          if (!(ok = ring_wait(&full_bar[r.slot], r.parity, &abort_flag, wait_ns))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t so = (uint64_t)((uint32_t)(r.slot * kPairStageBytes) >> 4);
@@ -879,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint16_t* res_src = ep.residual ? ep.residual + row0 * ep.ldr + col0 : nullptr;
         if (res_src && ep.vec) box_issue(res, res_src, ep.ldr, rows, cols, lane);
         if (c == 0) {
-          if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u, p.wait_ns) || abort_flag)) {
+          if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full[b], (uint32_t)(tc >> 1) & 1u, wait_ns) || abort_flag)) {
             gone = true;
             break;
           }
@@ -967,6 +971,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   if (abort_flag) {                                // the same in all threads of both CTAs
+    if (rank == 1 && warp == 0 && lane < 2)
+      st_cluster(mapa_shared(smem_u32(const_cast<int*>(&s_issued[2 + lane])), 0), (uint32_t)s_issued[2 + lane]);
+    __syncwarp();
+    cluster_sync_all();
     if (rank == 0 && warp == 0) pair_drain(full_bar, s_issued, (uint32_t)half * 128u, p.status, lane);
     cluster_sync_all();
   }
@@ -1144,10 +1152,11 @@ struct Product {
   Epilogue ep;
 };
 
-template <int ACT>
+template <int ACT, bool LIMIT = false>
 cudaError_t launch_split_act(const SplitParams& p, int smem, cudaStream_t st) {
+  if (!LIMIT && p.wait_ns != kWaitLimitNs) return launch_split_act<ACT, true>(p, smem, st);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_split_kernel<ACT>, done);
+  cudaError_t e = allow_smem(linear_split_kernel<ACT, LIMIT>, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.S * p.tiles));
@@ -1165,7 +1174,7 @@ cudaError_t launch_split_act(const SplitParams& p, int smem, cudaStream_t st) {
   attr[2].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<ACT>, p);
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<ACT, LIMIT>, p);
 }
 
 // ---------------------------------------------------------------- choice of kernel and tiles
@@ -1363,12 +1372,13 @@ cudaError_t launch_split(int act, const Product* prod, int n, const SplitPlan& p
   return cudaErrorInvalidValue;
 }
 
-template <int ACT>
+template <int ACT, bool LIMIT = false>
 cudaError_t launch_pair_act(const PairParams& p, int pairs, cudaStream_t st) {
+  if (!LIMIT && p.wait_ns != kWaitLimitNs) return launch_pair_act<ACT, true>(p, pairs, st);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_pair_kernel<ACT>, done);
+  cudaError_t e = allow_smem(linear_pair_kernel<ACT, LIMIT>, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(linear_pair_kernel<ACT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, p);
+  return launch_pdl(linear_pair_kernel<ACT, LIMIT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, p);
 }
 
 cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoin& db, uint32_t* status, bool clear,
