@@ -1267,6 +1267,10 @@ PairSchedule schedule_pairs(const long long* tiles, const double* cost, int pair
   return best;
 }
 
+// Pairs at work on two products' tiles: one for each tile of either, up to one
+// per two SMs.
+int pair_count(const long long* tiles) { return (int)std::min<long long>(kNumSMs / 2, tiles[0] + tiles[1]); }
+
 // A tile of the pair kernel: its products (a step takes longer the more pairs
 // are at work: L2 and power) and its epilogue, which run beside each other.
 struct PairTileUs {
@@ -1279,14 +1283,14 @@ PairTileUs pair_tile_us(const Product& q, int bn, double busy) {
   return {mma, std::max(mma, bn == 256 ? (maps ? 2.5 : 4.5) : (maps ? 1.5 : 2.5))};
 }
 double pair_us(const Product* prod, int n, int bn) {
-  constexpr int kPairs = kNumSMs / 2;
   long long tiles[2] = {0, 0}, steps = 0;
   for (int i = 0; i < n; ++i) {
     tiles[i] = ceil_div(prod[i].a.rows, kPairM) * ceil_div(prod[i].b.rows, bn);
     steps = std::max(steps, ceil_div(prod[i].red, kStepK));
   }
   const long long all = tiles[0] + tiles[1];
-  const double busy = (double)all / (ceil_div(all, kPairs) * kPairs);
+  const int pairs = pair_count(tiles);
+  const double busy = (double)all / (ceil_div(all, kNumSMs / 2) * (kNumSMs / 2));
   double mma[2] = {0, 0}, cost[2] = {0, 0};
   for (int i = 0; i < n; ++i) {
     const PairTileUs t = pair_tile_us(prod[i], bn, busy);
@@ -1294,7 +1298,7 @@ double pair_us(const Product* prod, int n, int bn) {
   }
   // filling and draining the pipeline costs less where a tile is a step or two
   const double ends = std::min(bn == 256 ? 7.6 : 6.0, 3.0 + 1.7 * steps);
-  return std::max(ends + schedule_pairs(tiles, mma, kPairs).end, 3.0 + schedule_pairs(tiles, cost, kPairs).end);
+  return std::max(ends + schedule_pairs(tiles, mma, pairs).end, 3.0 + schedule_pairs(tiles, cost, pairs).end);
 }
 
 struct Choice {
@@ -1387,7 +1391,6 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
   if (cleared != cudaSuccess) return cleared;
   PairParams p;
   memset(&p, 0, sizeof p);
-  constexpr int kPairs = kNumSMs / 2;
   long long tiles[2] = {0, 0};
   for (int i = 0; i < n; ++i) {
     PairProblem& q = p.prob[i];
@@ -1420,7 +1423,7 @@ cudaError_t launch_pair(int act, const Product* prod, int n, int bn, const DbJoi
   p.db = db;
   p.status = status;
   p.clear = clear;
-  const int pairs = (int)std::min<long long>(kPairs, std::max<long long>(tiles[0], tiles[1]));
+  const int pairs = pair_count(tiles);
   double cost[2] = {0, 0};
   for (int i = 0; i < n; ++i) cost[i] = pair_tile_us(prod[i], bn, 1).all;
   const PairSchedule plan = schedule_pairs(tiles, cost, pairs);
