@@ -657,20 +657,20 @@ int balance_rows_per_block(int T) {
   return max(kSumWarps, (T + kNumSMs - 1) / kNumSMs);
 }
 
-int balance_blocks(int T) {
-  if (T <= kBalanceSeqMaxT) return 0;
+int balance_blocks(int T, int E) {
+  if (balance_one_launch(T, E)) return 0;
   const int r = balance_rows_per_block(T);
   return (T + r - 1) / r;
 }
 
-int balance_scratch_blocks(int T) {
-  return T <= kBalanceSeqMaxT ? 0 : min(kNumSMs, (T + kSumWarps - 1) / kSumWarps);
+int balance_scratch_blocks(int T, int E) {
+  return balance_one_launch(T, E) ? 0 : min(kNumSMs, (T + kSumWarps - 1) / kSumWarps);
 }
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
                                 cudaStream_t st) {
-  const int blocks = T <= kBalanceManyMaxT && T <= kBalanceManyMean * (long long)B ? 0 : balance_blocks(T);
+  const int blocks = balance_by_sequence(T, E, B) ? 0 : balance_blocks(T, E);
   float* psum = static_cast<float*>(scratch);
   BalanceParams p{logits, ids, off, T, E, k, B, balance_rows_per_block(T), coef, psum,
                   reinterpret_cast<int*>(psum + (size_t)(blocks + B) * E), counts, mean, loss};

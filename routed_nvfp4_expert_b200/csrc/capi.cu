@@ -779,7 +779,7 @@ moe_status_t dense_ffn_bf16(int32_t H, int32_t I, float limit, const uint16_t* x
 
 size_t moe_balance_workspace_size(const moe_config_t* cfg, int32_t T, int32_t num_seqs) {
   if (check_cfg(cfg) != MOE_OK || check_T(T) != MOE_OK || check_seqs(nullptr, num_seqs, true) != MOE_OK) return 0;
-  const size_t blocks = rnx::balance_scratch_blocks(T);
+  const size_t blocks = rnx::balance_scratch_blocks(T, cfg->num_experts);
   return up(blocks ? 8 * (blocks + num_seqs) * (size_t)cfg->num_experts : 1);
 }
 

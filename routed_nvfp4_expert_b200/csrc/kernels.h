@@ -314,20 +314,36 @@ cudaError_t launch_w4a16_grouped_gemm(const W4a16GemmArgs& a, cudaStream_t st);
 
 // Inputs of up to this many tokens are summed by one CTA per sequence (one
 // launch, 6.9 us at 128 x 288); longer ones by one CTA per SM and a join (7.9
-// against 10.1 us at 256).
-constexpr int kBalanceSeqMaxT = 128;
+// against 10.1 us at 256). A CTA's time goes with rows times experts, so above
+// 288 experts this limit and the next two go down in proportion (128 x 1024: 15.7
+// us by one CTA, 8.3 by all SMs).
+constexpr int kBalanceSeqMaxT = 128, kBalanceExperts = 288;
+inline bool balance_one_launch(int T, int E) {
+  return T * std::max<long long>(E, kBalanceExperts) <= kBalanceSeqMaxT * kBalanceExperts;
+}
 // Many short sequences are too: the second form pays 1 to 3 us for every
 // sequence that ends inside a CTA's rows (62 sequences of 512 x 288 in all: 4.2
-// against 15.8 us; of 2048 x 288: 8.2 against 13.3 us). The host does not see
-// the lengths; were one sequence to hold all 2048 rows, it would take 47 us.
-constexpr int kBalanceManyMaxT = 2048, kBalanceManyMean = 64;
+// against 15.8 us). The host does not see the lengths, and one CTA for a long
+// sequence among empty ones costs as much as the many gain, or more: equal
+// sequences of 32 rows, and all rows in the first of as many, a CTA per sequence
+// against rows by SM, take (us)
+//   512 x 8    2.4, 6.3 and 4.6, 6.3     2048 x 8    2.5, 6.6 and 12.5, 7.4
+//   512 x 64   2.6, 5.9 and 8.1, 6.1     2048 x 64   2.7, 6.1 and 25.4, 6.5
+//   512 x 288  3.9, 6.4 and 16.4, 7.6    2048 x 288  4.0, 6.6 and 49.5, 9.4
+//   512 x 1024 7.0, 8.3 and 45.1, 9.8    2048 x 1024 7.1, 8.7 and 161, 15.7
+// so the limit is where the loss is as many times as the gain.
+constexpr int kBalanceManyMaxT = 512, kBalanceManyMean = 64;
+inline bool balance_by_sequence(int T, int E, int B) {
+  const long long most = kBalanceExperts, rows = T * std::max<long long>(E, most);
+  return rows <= kBalanceManyMaxT * most && rows <= kBalanceManyMean * most * B;
+}
 // CTAs of the first step of launch_balance_loss (0: the one-launch form), and
 // the most of any up to T tokens. Its scratch holds (the most + B) * E floats and
 // as many ints, so that fewer tokens never need more (2368 make 148 CTAs, 2369
 // make 140), nor fewer sequences (it is there also where many short ones leave
 // it unused).
-int balance_blocks(int T);
-int balance_scratch_blocks(int T);
+int balance_blocks(int T, int E);
+int balance_scratch_blocks(int T, int E);
 // off: [B + 1] ascending row offsets (NULL with B = 1: all T rows).
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, int T, int E, int k, const int32_t* off,
                                 int B, float coef, int32_t* counts, float* mean, float* loss, void* scratch,
