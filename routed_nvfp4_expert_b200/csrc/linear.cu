@@ -39,7 +39,8 @@ namespace {
 // of 1 + |z|, and the values within 2^-13 of themselves while Phi(z) or 1 / (1 + E)
 // is above 2^-126, a sixteenth of bf16's half step or less (below that, from z =
 // -13 in GELU, -10 in its tanh form and -87 in SiLU, they are 0). With E = 2^(-v log2 e) and s = 1 /
-// (1 + E), 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0.
+// (1 + E), 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0
+// (another keeps z^2 finite beside a factor of 0).
 
 RNX_DEVICE float pow2(float x) {
   float y;
@@ -97,7 +98,7 @@ RNX_DEVICE float act_grad(float z) {
     return fmaf(z * 0.3989422804014327f, g, cdf);
   }
   if (ACT == MOE_ACT_GELU_TANH) {
-    const float z2 = z * z, E = pow2(z * fmaf(-0.10294325f, z2, -2.3022082f)), s = recip(1.f + E);
+    const float z2 = fminf(z * z, 1e30f), E = pow2(z * fmaf(-0.10294325f, z2, -2.3022082f)), s = recip(1.f + E);
     return fmaf(z * s * fminf(E * s, 1.f), fmaf(0.21406445f, z2, 1.5957691f), s);
   }
   if (ACT == MOE_ACT_SILU) {

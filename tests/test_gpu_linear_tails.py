@@ -59,3 +59,20 @@ def test_slopes_in_the_tail(act):
     value, slope = _cdf(act, Z)
     ref = 0.5 * (value + Z * slope)
     assert float(((db.to(F64) - ref) / ref).abs().max()) <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("act", ["relu", *LOWEST])
+def test_far_out(act):
+    """Finite z of any size: the value is z or 0 and the slope 1 or 0, never NaN."""
+    far = torch.tensor([1e3, 1e6, 1e10, 1e19, 1e20, 1e30, 3e38]).to(BF16)
+    z = torch.cat([far, -far]).cuda()[None]
+    N = z.shape[1]
+    x, w = torch.ones(1, 8, dtype=BF16, device="cuda"), torch.ones(N, 8, dtype=BF16, device="cuda")
+    db = torch.empty(N, device="cuda")
+    capi.linear_bf16_backward(torch.ones_like(z), x, w, capi.alloc_linear_backward_workspace(z, x, w), z=z, act=act, db=db)
+    want = torch.cat([torch.ones(len(far)), torch.zeros(len(far))]).cuda()
+    assert torch.equal(db, want), db
+    x, w = torch.ones(1, 1, dtype=BF16, device="cuda"), z.T.contiguous()
+    y = torch.empty(1, N, dtype=BF16, device="cuda")
+    capi.linear_bf16(x, w, y, capi.alloc_linear_workspace(x, w), act=act)
+    assert torch.equal(y, torch.where(z > 0, z, torch.zeros_like(z))), y
