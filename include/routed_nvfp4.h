@@ -493,8 +493,9 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, const float* logits, c
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 } moe_act_t;
 
 /*
- * BF16 linear layer with a fused epilogue -- the product that dense_ffn_bf16
- * is built of, for every projection around the site:
+ * BF16 linear layer with a fused epilogue, for the projections around the site
+ * (dense_ffn_bf16 and the shared expert keep a product of their own, whose
+ * epilogue is the clamped SwiGLU of two of them):
  *   z = x w^T + bias;  y = act(z) + residual
  *   x bf16 [T, K], w bf16 [N, K], bias bf16 [N] or NULL, residual bf16 [T, N]
  *   or NULL, z_out bf16 [T, N] or NULL (the pre-activation, kept for
@@ -526,7 +527,8 @@ moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T,
  *   with MOE_ACT_NONE); dx bf16 [T, K], dw bf16 [N, K], db fp32 [N]: out, each
  *   may be NULL, not all (unless T = 0, where dx is empty). The residual's gradient is dy itself. dz enters the
  *   two products rounded to bf16 and db unrounded; accumulation is fp32.
- *   Pitches as above. T = 0 writes zeros to dw and db.
+ *   Pitches as above; no output may overlap an input or another output. T = 0
+ *   writes zeros to dw and db.
  *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above;
  *   here and in linear_bf16 fewer tokens of the same pitches never need more.
  */

@@ -14,8 +14,8 @@
 //   dx       m = k (W, MN-major),  j = t (dz, K-major),  r = n
 //   dW       m = k (x, MN-major),  j = n (dz, MN-major), r = t
 //
-// dz is rounded to bf16, the tensor cores' operand type (half a step, 2^-9 of
-// each element; y, z, dx and dW take the same one rounding); db is summed in
+// dz is rounded to bf16, the tensor cores' operand type (half a step, at most 2^-8
+// of each element; y, z, dx and dW take the same one rounding); db is summed in
 // fp32 from the unrounded dz.
 
 #include "common.cuh"
@@ -33,8 +33,8 @@ namespace {
 // next tile's products, and the dz pass as many as it streams, so their
 // instruction count matters: with normcdff, tanhf, expf and full divisions the
 // epilogue took longer than the products (60% of the tensor pipe at 4096 x 4096
-// x 12288, 85% now) and the dz pass 3.3 times its HBM time (now 1.5). Everything is put
-// on one power of two and one reciprocal (within 2^-22 each); GELU's normal
+// x 12288, 83% now) and the dz pass of 4096 x 12288 was bound by them (now 50 to 56
+// us for 46 us of HBM traffic). Everything is put on one power of two and one reciprocal (within 2^-22 each); GELU's normal
 // tail is a fit of this file (normal_cdf). All values and slopes stay within 2^-20
 // of 1 + |z|, and the values within 2^-13 of themselves while Phi(z) or 1 / (1 + E)
 // is above 2^-126, a sixteenth of bf16's half step or less (below that, from z =
