@@ -638,7 +638,7 @@ moe_status_t moe_set_stage_events(void* const* events, int32_t n);
  * Test hook of the failure path (not for production use; process-wide host
  * setting read at launch): the limit of the main-loop waits of the BF16
  * tensor-core GEMM (dense_ffn_bf16 / the shared expert at T >= 128, the
- * prefill router) and of linear_bf16 and its backward. ns >= 0 sets it (0 = a wait gives up as soon as it finds
+ * prefill router), of nvfp4_grouped_gemm and of linear_bf16 and its backward. ns >= 0 sets it (0 = a wait gives up as soon as it finds
  * the awaited copy or MMA still in flight); ns < 0 restores the default 2 s.
  * A wait that runs out sets MOE_ERR_DEVICE_TIMEOUT in the status word; the
  * kernel then issues nothing more, waits with the default limit for every copy

@@ -535,8 +535,8 @@ def moe_set_stage_events(events):
 
 
 def moe_set_wait_limit(ns: int):
-    """Test hook: limit of the main-loop waits of the BF16 tensor-core GEMM and
-    the BF16 linear layer (ns < 0 restores the default)."""
+    """Test hook: limit of the main-loop waits of the BF16 tensor-core GEMM, the
+    FP4 pair GEMM and the BF16 linear layer (ns < 0 restores the default)."""
     _check(lib().moe_set_wait_limit(int(ns)))
 
 

@@ -33,7 +33,8 @@
 // quadrant w % 4 and one half of the 256 accumulator columns, copies them to
 // registers and releases the accumulator with a CTA-scope arrive before the
 // SwiGLU / scaling and the stores). Every wait is bounded; a
-// timeout sets the device status word and winds the pair down. No TMA load
+// timeout sets the device status word and winds the pair down once its copies
+// have landed (pair_drain). No TMA load
 // uses cluster multicast (only the MMA completion commit is multicast).
 
 #include "common.cuh"
@@ -95,6 +96,7 @@ struct PairParams {
   uint32_t* status;
   int E, K, out_cols, bank_rows;
   float limit;
+  unsigned long long wait_ns;    // with LIMIT, of the main-loop waits (the others keep the default)
 };
 
 // largest e with tile_offsets[e] <= mt. SMEM: the table was copied to shared
@@ -133,9 +135,11 @@ __device__ __forceinline__ void store_rows_256(const uint8_t* area, float* dst, 
   __syncwarp();
 }
 
-template <bool GATE_UP>
+// LIMIT: for a test's limit on the waits.
+template <bool GATE_UP, bool LIMIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_pair_gemm_kernel(const __grid_constant__ PairParams p) {
+  const unsigned long long wait_ns = LIMIT ? p.wait_ns : kWaitLimitNs;
   constexpr int kS = stages_of<GATE_UP>();
   constexpr int kEpiStage = epi_stage_bytes_of<GATE_UP>();
   extern __shared__ uint8_t smem_raw[];
@@ -143,7 +147,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full_bar[kS], empty_bar[kS];
   __shared__ __align__(8) uint64_t acc_full, acc_empty, mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag;     // of both CTAs: set in each by whoever stops
+  __shared__ volatile int s_issued[2];    // steps by the even and by the odd CTA's producer
   __shared__ int s_toff[GATE_UP ? 1 : kMaxExperts + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -192,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int ks = 0; ks < n_ksteps; ++ks, ++it) {
         const int s = it % kS;
         const uint32_t ph = (uint32_t)(it / kS) & 1u;
-        if (__any_sync(0xffffffffu, !mbar_wait_poll(&empty_bar[s], ph ^ 1u) || abort_flag)) {
+        if (__any_sync(0xffffffffu, !mbar_wait_poll(&empty_bar[s], ph ^ 1u, wait_ns) || abort_flag)) {
           ok = false;
           break;
         }
@@ -229,15 +234,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
-      set_status(p.status, kDevErrTimeout);
-      abort_flag = 1;
+    if (lane == 0) {
+      if (!ok) stop_pair(p.status, &abort_flag);
+      s_issued[rank] = it;
     }
-    // drain (even CTA: its full barriers count both CTAs' bytes)
-    if (rank == 0)
-      for (int j = max(0, it - kS); j < it; ++j)
-        if (!mbar_wait(&full_bar[j % kS], (uint32_t)(j / kS) & 1u) && lane == 0)
-          set_status(p.status, kDevErrTimeout);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     // Whole warp in the loop, one elected lane issues; the descriptors of
@@ -252,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = pair; tile < n_tiles && ok; tile += n_pairs, ++tc) {
         // both CTAs' epilogues must have drained the accumulator of the previous tile
-        if (__any_sync(0xffffffffu, !mbar_wait_cluster(&acc_empty, ((uint32_t)tc & 1u) ^ 1u))) {
+        if (__any_sync(0xffffffffu, !mbar_wait_cluster(&acc_empty, ((uint32_t)tc & 1u) ^ 1u, wait_ns))) {
           ok = false;
           break;
         }
@@ -260,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < n_ksteps; ++ks, ++it) {
           const int s = it % kS;
           const uint32_t ph = (uint32_t)(it / kS) & 1u;
-          if (__any_sync(0xffffffffu, !mbar_wait_poll(&full_bar[s], ph) || abort_flag)) {
+          if (__any_sync(0xffffffffu, !mbar_wait_poll(&full_bar[s], ph, wait_ns) || abort_flag)) {
             ok = false;
             break;
           }
@@ -298,10 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (elect_one()) mma_commit_pair_mc(&acc_full, 0x3);   // accumulator final in both CTAs
         __syncwarp();
       }
-      if (!ok && lane == 0) {
-        set_status(p.status, kDevErrTimeout);
-        abort_flag = 1;
-      }
+      if (!ok && lane == 0) stop_pair(p.status, &abort_flag);
       if (elect_one()) mma_commit_pair_mc(&mma_done, 0x1);
       __syncwarp();
       if (!mbar_wait(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
@@ -356,11 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         w_cur = weight_of(m_next);
         m_next = meta_of(tile + 2 * n_pairs);
       };
-      if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full, (uint32_t)tc & 1u) || abort_flag)) {
-        if (lane == 0) {
-          set_status(p.status, kDevErrTimeout);
-          abort_flag = 1;
-        }
+      if (__any_sync(0xffffffffu, !mbar_wait_poll(&acc_full, (uint32_t)tc & 1u, wait_ns) || abort_flag)) {
+        if (lane == 0) stop_pair(p.status, &abort_flag);
         break;
       }
       tc_fence_after();
@@ -438,10 +432,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // no CTA leaves (or frees TMEM) while the pair's MMAs or copies may still
-  // touch its shared or tensor memory
+  // touch its shared or tensor memory; without an abort the products have
+  // consumed every copy
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
+  if (abort_flag) {                       // the same in all threads of both CTAs
+    const uint32_t bytes[2] = {kStageBytes, kStageBytes};
+    pair_drain<2, kS>(rank, full_bar, s_issued, bytes, p.status);
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
@@ -495,13 +494,16 @@ cudaError_t launch_fp4_grouped_gemm(const Fp4GemmArgs& a, cudaStream_t st) {
   p.out_cols = a.out_cols;
   p.bank_rows = a.bank_rows;
   p.limit = a.limit;
-  auto kern = gu ? fp4_pair_gemm_kernel<true> : fp4_pair_gemm_kernel<false>;
+  p.wait_ns = test_wait_limit_ns();
+  const bool limit = p.wait_ns != kWaitLimitNs;
+  auto kern = gu ? (limit ? fp4_pair_gemm_kernel<true, true> : fp4_pair_gemm_kernel<true, false>)
+                 : (limit ? fp4_pair_gemm_kernel<false, true> : fp4_pair_gemm_kernel<false, false>);
   const int smem_bytes = gu ? smem_bytes_of<true>() : smem_bytes_of<false>();
-  static bool attr_done[2] = {false, false};
-  if (!attr_done[gu]) {
+  static bool attr_done[2][2] = {};
+  if (!attr_done[gu][limit]) {
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
     if (err != cudaSuccess) return err;
-    attr_done[gu] = true;
+    attr_done[gu][limit] = true;
   }
   kern<<<kNumSMs, kThreads, smem_bytes, st>>>(p);   // 74 clusters of 2 (compile-time cluster shape)
   return cudaGetLastError();

@@ -534,13 +534,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // which one tensor store writes them (the lanes' own stores where the pitch or N
 // is no multiple of 8 elements).
 // Every wait is bounded. No TMA load uses cluster multicast.
-//
-// A wait that runs out stops both CTAs, and the four producers may stop at
-// different steps: a step that only some of them issued would leave its copies
-// on the way, to either CTA, with a barrier that never completes. So each
-// producer leaves its count of issued steps, and once everything has stopped the
-// even CTA collects them, counts the missing bytes as if they had come and waits
-// for the rest (pair_drain); only then do the CTAs leave.
 
 constexpr int kPairM = 256;
 constexpr int kPairStages = 6;
@@ -707,28 +700,6 @@ RNX_DEVICE void box_load_any(uint8_t* box, const uint16_t* src, long long ld, in
   __syncwarp();
 }
 
-// Ends the copies of a pair that stopped early (one warp of the even CTA, when no
-// producer issues any more and every MMA is done). issued: steps by A and B of the
-// even, then of the odd CTA. No producer is ahead of another by more than the
-// ring, since a slot is freed by the products of a step that all four issued.
-RNX_DEVICE void pair_drain(uint64_t* full_bar, const volatile int* issued, uint32_t b_bytes, uint32_t* status, int lane) {
-  int first = issued[0], last = issued[0];
-  for (int i = 1; i < 4; ++i) first = min(first, issued[i]), last = max(last, issued[i]);
-  if (lane == 0) {
-    for (int step = first; step < last; ++step) {
-      uint64_t* bar = &full_bar[step % kPairStages];
-      if (issued[0] <= step) mbar_arrive_expect_tx(bar, 2u * (kABytes + b_bytes));   // the one that announces the bytes
-      for (int i = 0; i < 4; ++i)
-        if (issued[i] <= step) mbar_complete_tx(bar, i % 2 ? b_bytes : (uint32_t)kABytes);
-    }
-  }
-  __syncwarp();
-  for (int step = max(0, last - kPairStages); step < last; ++step)
-    if (!mbar_wait(&full_bar[step % kPairStages], (uint32_t)(step / kPairStages) & 1u) && lane == 0)
-      set_status(status, kDevErrTimeout);
-  __syncwarp();
-}
-
 template <int ACT, bool LIMIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
@@ -739,16 +710,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int abort_flag;              // of both CTAs: set in each by whoever stops
-  __shared__ volatile int s_issued[4];             // steps by A and B of the even, then of the odd CTA: its own here
+  __shared__ volatile int s_issued[4];             // steps by A and B of the even, then of the odd CTA
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag));
-  auto stop_pair = [&] {                           // one lane; before the closing cluster_sync_all
-    set_status(p.status, kDevErrTimeout);
-    st_cluster(mapa_shared(abort_at, 0), 1u);
-    st_cluster(mapa_shared(abort_at, 1), 1u);
-  };
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int half = p.bn / 2;                       // this CTA's rows of B
 
@@ -811,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     if (lane == 0) {
-      if (!ok) stop_pair();
+      if (!ok) stop_pair(p.status, &abort_flag);
       s_issued[2 * rank + !is_a] = issued;
     }
   } else if (warp == 1) {
@@ -848,7 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (elect_one()) mma_commit_pair_mc(&acc_full[b], 0x3);
         __syncwarp();
       }
-      if (!ok && lane == 0) stop_pair();
+      if (!ok && lane == 0) stop_pair(p.status, &abort_flag);
       if (elect_one()) mma_commit_pair_mc(&mma_done, 0x1);
       __syncwarp();
       if (!mbar_wait(&mma_done, 0) && lane == 0) set_status(p.status, kDevErrTimeout);
@@ -958,7 +923,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         box_store<kBoxUnroll>(box, &q.tma_out, ep.out, ep.ldo, row0, col0, rows, cols, ep.vec, lane);
       }
       if (gone) {
-        if (lane == 0) stop_pair();
+        if (lane == 0) stop_pair(p.status, &abort_flag);
         break;
       }
     }
@@ -972,12 +937,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   if (abort_flag) {                                // the same in all threads of both CTAs
-    if (rank == 1 && warp == 0 && lane < 2)
-      st_cluster(mapa_shared(smem_u32(const_cast<int*>(&s_issued[2 + lane])), 0), (uint32_t)s_issued[2 + lane]);
-    __syncwarp();
-    cluster_sync_all();
-    if (rank == 0 && warp == 0) pair_drain(full_bar, s_issued, (uint32_t)half * 128u, p.status, lane);
-    cluster_sync_all();
+    const uint32_t b_bytes = (uint32_t)half * 128u, bytes[4] = {kABytes, b_bytes, kABytes, b_bytes};
+    pair_drain<4, kPairStages>(rank, full_bar, s_issued, bytes, p.status);
   }
   if (warp == 2) {
     tc_fence_after();

@@ -298,4 +298,56 @@ RNX_DEVICE void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y
       : "memory");
 }
 
+// ---------------------------------------------------------------- a pair that stops early
+// A wait that runs out stops both CTAs of a pair, and their producers may stop
+// at different steps: a step that only some of them issued would leave its
+// copies on the way, to either CTA, with a barrier that never completes. So each
+// producer leaves its count of issued steps in its own CTA, and once everything
+// has stopped the even CTA collects them, counts the missing bytes as if they had
+// come and waits for the rest; only then do the CTAs leave.
+
+// By one lane, before the pair's closing cluster_sync_all: the abort flag of both.
+RNX_DEVICE void stop_pair(uint32_t* status, volatile int* abort_flag) {
+  set_status(status, kDevErrTimeout);
+  const uint32_t at = smem_u32(const_cast<int*>(abort_flag));
+  st_cluster(mapa_shared(at, 0), 1u);
+  st_cluster(mapa_shared(at, 1), 1u);
+}
+
+// By all threads of both CTAs behind that barrier, when no producer issues any
+// more, every MMA is done and the flag is set. issued: steps by PRODUCERS
+// producers, the even CTA's first (each CTA has set its own), whose first announces
+// a step's bytes; bytes: of a step by each producer. No producer is ahead of
+// another by more than the ring, since a slot is freed by the products of a step
+// that all issued.
+template <int PRODUCERS, int STAGES>
+RNX_DEVICE void pair_drain(uint32_t rank, uint64_t* full_bar, volatile int* issued, const uint32_t (&bytes)[PRODUCERS],
+                           uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kMine = PRODUCERS / 2;
+  if (rank == 1 && threadIdx.x < kMine)
+    st_cluster(mapa_shared(smem_u32(const_cast<int*>(issued + kMine + threadIdx.x)), 0), (uint32_t)issued[kMine + threadIdx.x]);
+  __syncwarp();
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x < 32) {
+    int first = issued[0], last = issued[0];
+    uint32_t all = bytes[0];
+    for (int i = 1; i < PRODUCERS; ++i) first = min(first, issued[i]), last = max(last, issued[i]), all += bytes[i];
+    if (lane == 0) {
+      for (int step = first; step < last; ++step) {
+        uint64_t* bar = &full_bar[step % STAGES];
+        if (issued[0] <= step) mbar_arrive_expect_tx(bar, all);
+        for (int i = 0; i < PRODUCERS; ++i)
+          if (issued[i] <= step) mbar_complete_tx(bar, bytes[i]);
+      }
+    }
+    __syncwarp();
+    for (int step = max(0, last - STAGES); step < last; ++step)
+      if (!mbar_wait(&full_bar[step % STAGES], (uint32_t)(step / STAGES) & 1u) && lane == 0)
+        set_status(status, kDevErrTimeout);
+    __syncwarp();
+  }
+  cluster_sync_all();
+}
+
 }  // namespace rnx
