@@ -525,8 +525,9 @@ moe_status_t linear_bf16(int32_t act, const uint16_t* x, int64_t ldx, int32_t T,
  *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  db = sum_t dz
  *   dy bf16 [T, N]; z bf16 [T, N], the pre-activation linear_bf16 kept (NULL
  *   with MOE_ACT_NONE); dx bf16 [T, K], dw bf16 [N, K], db fp32 [N]: out, each
- *   may be NULL, not all (unless T = 0, where dx is empty). The residual's gradient is dy itself. dz enters the
- *   two products rounded to bf16 and db unrounded; accumulation is fp32.
+ *   may be NULL, not all (unless T = 0, where dx is empty). The residual's
+ *   gradient is dy itself. dz enters the two products rounded to bf16 and db
+ *   unrounded; accumulation is fp32.
  *   Pitches as above; no output may overlap an input or another output. T = 0
  *   writes zeros to dw and db.
  *   ws: linear_backward_workspace_size(T, K, N, ldx, ldw) bytes, as above;
@@ -638,8 +639,9 @@ moe_status_t moe_set_stage_events(void* const* events, int32_t n);
  * Test hook of the failure path (not for production use; process-wide host
  * setting read at launch): the limit of the main-loop waits of the BF16
  * tensor-core GEMM (dense_ffn_bf16 / the shared expert at T >= 128, the
- * prefill router), of nvfp4_grouped_gemm and of linear_bf16 and its backward. ns >= 0 sets it (0 = a wait gives up as soon as it finds
- * the awaited copy or MMA still in flight); ns < 0 restores the default 2 s.
+ * prefill router), of nvfp4_grouped_gemm and of linear_bf16 and its backward.
+ * ns >= 0 sets it (0 = a wait gives up as soon as it finds the awaited copy or
+ * MMA still in flight); ns < 0 restores the default 2 s.
  * A wait that runs out sets MOE_ERR_DEVICE_TIMEOUT in the status word; the
  * kernel then issues nothing more, waits with the default limit for every copy
  * and MMA it already issued, frees its tensor memory and returns, so later

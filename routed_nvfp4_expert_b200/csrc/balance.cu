@@ -391,12 +391,15 @@ struct GradParams {
 };
 
 // Both means are sums of products with scores that may be as small as 2^-126,
-// divided by a sum of such scores: the other factor is raised by 2^40 for the
-// sum (exact; factors from 2^-40 to 2^87 keep their accuracy beside any
-// score) and lowered again behind the division. Every gradient is formed as
-// (slope / sum of scores) (upstream times difference): the first factor is at
-// most 1, while the sum's reciprocal alone reaches 2^126.
+// divided by a sum of such scores: the other factor is raised for the sum by a
+// power of two, and lowered again behind the division. Gradients of the weights
+// are raised by 2^40 (from 2^-40 to 2^87 they keep their accuracy beside any
+// score); loads f, at least 2^-22, by 2^24, which the balance loss's factor takes
+// back (from 2^-102 on it is exact). Every gradient is formed as (slope / sum of
+// scores) (upstream times difference): the first factor is at most 1, while the
+// sum's reciprocal alone reaches 2^126.
 constexpr float kRaise = 1099511627776.f, kLower = 1.f / kRaise;
+constexpr float kRaiseLoad = 16777216.f, kLowerGain = 1.f / kRaiseLoad;
 
 // G lanes per row, each warp a run of consecutive rows, so that the loads f of
 // its sequence stay in registers. The routing weights' part of a row is k
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
   int b = seq_of_row(p.off, p.B, p.T, base);
   int start = b < p.B ? seq_start(p.off, b, p.T) : p.T, end = b < p.B ? seq_start(p.off, b + 1, p.T) : p.T;
   bool fresh = true;
-  float f[4 * NQ], gain = 0.f;                   // f times 2^40, gain times 2^-40
+  float f[4 * NQ], gain = 0.f;                   // f times 2^24, gain times 2^-24
 #pragma unroll
   for (int i = 0; i < 4 * NQ; ++i) f[i] = 0.f;
   for (int at = 0; base < r1; base += R, at = at == DEPTH - 1 ? 0 : at + 1) {
@@ -448,8 +451,8 @@ __global__ void __launch_bounds__(kGradWarps * 32, 2) router_grad_kernel(const G
     if (inside && fresh && p.d_loss) {
       fresh = false;
       const float n = (float)(end - start);
-      gain = p.d_loss[b] * p.coef / n * kLower;
-      const float fs = kRaise * ((float)E / ((float)k * n));
+      gain = p.d_loss[b] * p.coef / n * kLowerGain;
+      const float fs = kRaiseLoad * ((float)E / ((float)k * n));
       const int32_t* count = p.counts + (size_t)b * E;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {

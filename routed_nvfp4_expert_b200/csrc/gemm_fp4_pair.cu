@@ -34,8 +34,8 @@
 // registers and releases the accumulator with a CTA-scope arrive before the
 // SwiGLU / scaling and the stores). Every wait is bounded; a
 // timeout sets the device status word and winds the pair down once its copies
-// have landed (pair_drain). No TMA load
-// uses cluster multicast (only the MMA completion commit is multicast).
+// have landed (pair_drain). No TMA load uses cluster multicast (only the MMA
+// completion commit is multicast).
 
 #include "common.cuh"
 #include "kernels.h"

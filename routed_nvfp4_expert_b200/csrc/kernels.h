@@ -195,9 +195,9 @@ cudaError_t launch_dense_gemv(int H, int I, float limit, const uint16_t* x, int 
 cudaError_t launch_bf16_gemm(bool gate_up, const uint16_t* a, int M, int K, const uint16_t* b0, const uint16_t* b1,
                              int N, float limit, uint16_t* out, uint32_t* status, cudaStream_t st,
                              float* out_f32 = nullptr, bool split = false);
-// Limit of the main-loop waits of the BF16 GEMM and the BF16 linear layer for
-// later launches (host setting; 0 = give up at the first incomplete poll). Test
-// hook for the timeout path.
+// Limit of the main-loop waits of the BF16 GEMM, the FP4 pair GEMM and the BF16
+// linear layer for later launches (host setting; 0 = give up at the first
+// incomplete poll). Test hook for the timeout path.
 void set_test_wait_limit_ns(unsigned long long ns);
 unsigned long long test_wait_limit_ns();
 

@@ -34,11 +34,12 @@ namespace {
 // instruction count matters: with normcdff, tanhf, expf and full divisions the
 // epilogue took longer than the products (60% of the tensor pipe at 4096 x 4096
 // x 12288, 83% now) and the dz pass of 4096 x 12288 was bound by them (now 50 to 56
-// us for 46 us of HBM traffic). Everything is put on one power of two and one reciprocal (within 2^-22 each); GELU's normal
-// tail is a fit of this file (normal_cdf). All values and slopes stay within 2^-20
-// of 1 + |z|, and the values within 2^-13 of themselves while Phi(z) or 1 / (1 + E)
-// is above 2^-126, a sixteenth of bf16's half step or less (below that, from z =
-// -13 in GELU, -10 in its tanh form and -87 in SiLU, they are 0). With E = 2^(-v log2 e) and s = 1 /
+// us for 46 us of HBM traffic). Everything is put on one power of two and one
+// reciprocal (within 2^-22 each); GELU's normal tail is a fit of this file
+// (normal_cdf). All values and slopes stay within 2^-20 of 1 + |z|, and the values
+// within 2^-13 of themselves while Phi(z) or 1 / (1 + E) is above 2^-126, a
+// sixteenth of bf16's half step or less (below that, from z = -13 in GELU, -10 in
+// its tanh form and -87 in SiLU, they are 0). With E = 2^(-v log2 e) and s = 1 /
 // (1 + E), 1 - s = E s; the minimum puts it to 1 where E is infinite and s is 0
 // (another keeps z^2 finite beside a factor of 0).
 
@@ -70,7 +71,11 @@ RNX_DEVICE uint32_t pack2(float lo, float hi) {
 // = -8.)
 RNX_DEVICE float normal_cdf(float z, float& g) {
   const float t = recip(fmaf(0.29f, fabsf(z), 1.f));
-  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, -0.088841276f, 0.284976389f), -0.093334857f), 0.179639302f), 0.100685080f), 0.116875408f);
+  float poly = fmaf(t, -0.088841276f, 0.284976389f);
+  poly = fmaf(t, poly, -0.093334857f);
+  poly = fmaf(t, poly, 0.179639302f);
+  poly = fmaf(t, poly, 0.100685080f);
+  poly = t * fmaf(t, poly, 0.116875408f);
   g = pow2(-0.72134752f * z * z);
   const float tail = poly * g;
   return z > 0.f ? 1.f - tail : tail;
@@ -252,9 +257,8 @@ RNX_DEVICE void join_db(const DbJoin& d, int unit, int units, int lane) {
 // sent, 4.3 us read; 128 x 4096 x 4096, 128 columns: 16.2 us sent, 13.3 us
 // read.) A barrier that each thread arrives at behind its last store, and waits
 // for at its end, keeps every CTA until no peer has anything left to send it.
-// Up to two products share a
-// launch (dx and dW of few tokens); a reduction of fewer steps than S leaves
-// the last ranks without a part of their own.
+// Up to two products share a launch (dx and dW of few tokens); a reduction of
+// fewer steps than S leaves the last ranks without a part of their own.
 // Warps: 0 = TMA producer, 1 = MMA issuer, 2 = TMEM allocator, 3-7 = db join,
 // 4-7 = TMEM readers; all eight reduce and store. Every wait is bounded; a
 // timeout sets the status word, and the CTA still sends its (unspecified) part

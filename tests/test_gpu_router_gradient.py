@@ -169,3 +169,17 @@ def test_a_large_scaling_factor_at_the_lowest_scores():
     # m = 1.5
     want = rsf / 4 * (v.double() - v.double().mean(1, keepdim=True))
     assert ((out[:, :k] - want).abs() <= 1e-5 * rsf).all() and not out[:, k:].any()
+
+
+@pytest.mark.parametrize("E,k", [(40, 4), (288, 8)])
+def test_a_very_small_loss_gradient(E, k):
+    """The balance loss's factor is scaled inside; a gradient of 1e-28 keeps its accuracy."""
+    T = 64
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn(T, E, generator=g)
+    ids = torch.rand(T, E, generator=g).topk(k, dim=1).indices.to(torch.int32)
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E).to(torch.int32)[None]
+    d_loss = torch.tensor([1e-28])
+    bal, mag = _loss_gradient(logits, counts, k, 0.5, d_loss)
+    out = _call(logits, ids, k, counts=counts, coef=0.5, d_loss=d_loss)
+    assert ((out - bal).abs() <= _tol(E, logits) * mag + 1e-40).all()
