@@ -64,11 +64,11 @@ RNX_DEVICE uint32_t pack2(float lo, float hi) {
 
 // Phi(z), with g = exp(-z^2 / 2): Phi(-|z|) = g t P(t), t = 1 / (1 + 0.29 |z|).
 // P is the polynomial of degree 5 whose largest error over 0 <= |z| <= 14 is
-// least, by linear programming on 800 Chebyshev points, with the error of Phi
-// weighed as the smaller of absolute and 1000 times relative: 4.5e-8 absolute,
-// 9e-5 relative in the tail. (Approximations of erfc that bound the absolute
-// error alone, 7.5e-8 with a polynomial shorter by one, are off by 1% of y at z
-// = -8.)
+// least, by linear programming on 800 Chebyshev points, where an error of Phi
+// counts as twice itself or, where that is more, as a thousandth of its share of
+// Phi: 4.5e-8 in all, 9e-5 of Phi in the tail. (Approximations of erfc that bound
+// the error alone, 7.5e-8 with a polynomial shorter by one, are off by 1% of y at
+// z = -8.)
 RNX_DEVICE float normal_cdf(float z, float& g) {
   const float t = recip(fmaf(0.29f, fabsf(z), 1.f));
   float poly = fmaf(t, -0.088841276f, 0.284976389f);
